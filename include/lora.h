@@ -74,6 +74,13 @@ typedef enum {
 #define LORA_DEV_BAD_RANK 8     /* a retained rank outside [0, r_max]            */
 #define LORA_DEV_TIMEOUT 16     /* a bounded on-chip wait gave up                */
 
+/* Further bits, set by lora_kv_append (status_dev) and in the attention
+ * plan's status word (lora_attn_plan_status). */
+#define LORA_DEV_BAD_SLOT 32      /* a cache slot outside [-1, num_pages * page_size)  */
+#define LORA_DEV_BAD_POSITION 64  /* a position outside the rotation table             */
+#define LORA_DEV_BAD_PAGE 128     /* a page id outside [0, num_pages)                  */
+#define LORA_DEV_BAD_LENGTH 256   /* a length or row pointer that does not fit         */
+
 /* Limits of this implementation. */
 #define LORA_MAX_RANK 64          /* r_max                                    */
 #define LORA_MAX_CAPACITY 49152   /* adapters per pool / mapping key range    */
@@ -463,6 +470,173 @@ lora_status lora_rank_allocate(const float *sigma_host, int M, int r_stride, con
  * Returns LORA_ERR_INVALID_ARG for other kinds or limits.
  */
 lora_status lora_diag_wait_expiry(int kind, long long limit_ns, int32_t *words_dev, lora_stream_t stream);
+
+/*
+ * The attention step around the projections: keys and values of the batch's
+ * tokens appended to a paged cache (lora_kv_append), attention over that
+ * cache with prefixes shared by groups of requests (lora_prefix_attention),
+ * and the choice of the next tokens from the logits (lora_sample).  The
+ * pages hold adapters and the KV cache in one device pool and let requests
+ * of one adapter share the cached KV of a common prefix, whose values depend
+ * on the adapter (ELORA page, Sec. 1.2 - 1.3 and the dependency tree); they
+ * give no kernels for it.
+ *
+ * lora_kv_cache_create: a descriptor of a paged cache in the caller's memory
+ * (the storage is not owned: keep it alive until the descriptor is destroyed).
+ *   k_dev, v_dev : device bf16 [num_pages][n_kv_heads][page_size][head_dim],
+ *                  16-byte aligned: one head's part of a page is contiguous
+ *   page_size    : 16, 32, 64 or 128 tokens;  head_dim : 64 or 128
+ *   num_pages >= 1, n_kv_heads 1 .. LORA_MAX_KV_HEADS;
+ *   num_pages * n_kv_heads * page_size < 2^31 (else LORA_ERR_NOT_SUPPORTED)
+ * Slot s of the cache is token s % page_size of page s / page_size.
+ * Host only; lora_kv_cache_destroy(NULL) is a no-op.  Destroy a cache only
+ * after the work that uses it has finished.
+ */
+#define LORA_MAX_KV_HEADS 256
+typedef struct lora_kv_cache lora_kv_cache;
+lora_status lora_kv_cache_create(int num_pages, int page_size, int n_kv_heads, int head_dim, void *k_dev, void *v_dev,
+                                 lora_kv_cache **out);
+lora_status lora_kv_cache_destroy(lora_kv_cache *cache);
+
+/*
+ * lora_kv_append: writes T tokens' keys and values into the cache, the keys
+ * rotated by their positions, and rotates their queries on the way.
+ *   k_dev, v_dev : device bf16, token t's n_kv_heads x head_dim elements at
+ *                  t * k_stride (v_stride) elements: slices of a fused
+ *                  projection's output go in as they are
+ *   q_dev        : NULL, or device bf16, n_q_heads x head_dim elements per
+ *                  token at q_stride; q_out_dev (out_stride) receives the
+ *                  rotated queries and may be q_dev itself (same stride)
+ *   slots_dev    : device int32 [T], the cache slot of each token; -1 leaves
+ *                  the token's k and v out (padding).  Slots of one call are
+ *                  distinct.
+ *   rope_dev     : device fp32 [max_position][rot_dim]: rot_dim / 2 cosines,
+ *                  then rot_dim / 2 sines per position (NULL with rot_dim 0:
+ *                  nothing is rotated)
+ *   positions_dev: device int32 [T] (NULL with rot_dim 0)
+ *   rot_dim      : 0, or a multiple of 16 up to head_dim: the first rot_dim
+ *                  elements of a head are rotated, the others copied
+ *   style        : LORA_ROPE_HALVES pairs element i with i + rot_dim / 2,
+ *                  LORA_ROPE_ADJACENT pairs 2i with 2i + 1; the pair (a, b)
+ *                  becomes (a c - b s, b c + a s) in fp32, rounded once
+ *   status_dev   : NULL, or a device int32 that receives bits by atomic or
+ *                  (the caller clears it): LORA_DEV_BAD_SLOT (the token's k
+ *                  and v are left out), LORA_DEV_BAD_POSITION (the token is
+ *                  left out altogether: no k, v or q written)
+ * Pointers 16-byte aligned, strides multiples of 8 elements and at least
+ * the row's length; n_q_heads 1 .. LORA_MAX_Q_HEADS with a query.  The
+ * outputs overlap no input but q_dev.  T = 0 does nothing.  Stream-ordered,
+ * no allocation: safe to capture in a CUDA graph.
+ */
+#define LORA_MAX_Q_HEADS 1024
+#define LORA_ROPE_HALVES 0
+#define LORA_ROPE_ADJACENT 1
+lora_status lora_kv_append(const lora_kv_cache *cache, const void *k_dev, long long k_stride, const void *v_dev,
+                           long long v_stride, const void *q_dev, long long q_stride, void *q_out_dev,
+                           long long out_stride, int n_q_heads, const int32_t *slots_dev, const int32_t *positions_dev,
+                           const float *rope_dev, int max_position, int rot_dim, int style, int T,
+                           int32_t *status_dev, lora_stream_t stream);
+
+/*
+ * lora_attn_plan_create: device workspace of lora_prefix_attention for
+ * batches of up to max_requests requests with max_queries query tokens in
+ * all, in up to max_groups groups sharing a prefix each (0: no prefixes),
+ * whose prefixes and own parts take up to max_prefix_pages and
+ * max_suffix_pages pages.  Holds the batch's lengths and page tables, the
+ * schedule of the work over the SMs and the partial results.  Synchronous.
+ *   n_q_heads a multiple of n_kv_heads; head_dim and page_size as the cache's
+ *   max_requests, max_queries >= 1; each at most LORA_MAX_TOKENS
+ */
+typedef struct lora_attn_plan lora_attn_plan;
+lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_queries, int max_prefix_pages,
+                                  int max_suffix_pages, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                  lora_attn_plan **out);
+
+/*
+ * lora_attn_plan_build: takes a batch's layout.  One plan serves every
+ * lora_prefix_attention on the same batch (all layers, each with a cache of
+ * its own that is laid out alike).
+ *   q_offsets_dev : int32 [B+1], row pointer of each request's query tokens
+ *                   (0 or more each), up to TQ
+ *   suffix_len_dev: int32 [B], the request's own tokens in the cache: the
+ *                   ones after the shared prefix, its query tokens (the last
+ *                   ones) among them
+ *   suffix_pages_dev : int32 [B][suffix_stride], their pages in order
+ *   group_offsets_dev: int32 [NG+1], row pointer of each group's requests,
+ *                   up to B (requests of a group are consecutive)
+ *   prefix_len_dev: int32 [NG], tokens of the group's shared prefix (0: none)
+ *   prefix_pages_dev : int32 [NG][prefix_stride], its pages
+ *   NG = 0 (the three group arrays NULL): no request has a prefix
+ *   num_pages     : pages of the caches that will be read
+ * Query i of a request with n queries sees the whole prefix and the first
+ * suffix_len - n + i + 1 of its own tokens.  What only the device can see
+ * sets bits of the plan's status word, which this call clears: malformed
+ * row pointers empty the batch (or its prefixes), a length below 0 or above
+ * its table counts as 0 (LORA_DEV_BAD_LENGTH), a page id outside
+ * [0, num_pages) hides that page's keys (LORA_DEV_BAD_PAGE).
+ * Stream-ordered, no allocation; the arrays need to stay valid only until
+ * the stream reaches this call.
+ */
+lora_status lora_attn_plan_build(lora_attn_plan *plan, const int32_t *q_offsets_dev, const int32_t *suffix_len_dev,
+                                 const int32_t *suffix_pages_dev, int suffix_stride, const int32_t *group_offsets_dev,
+                                 const int32_t *prefix_len_dev, const int32_t *prefix_pages_dev, int prefix_stride,
+                                 int B, int NG, int TQ, int num_pages, lora_stream_t stream);
+
+/*
+ * lora_prefix_attention: for every query token and head,
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j)
+ * over the keys j it sees; a group's prefix is read once for all of the
+ * group's requests.  Query head h reads key/value head h / (n_q_heads /
+ * n_kv_heads).  A query that sees no key gives out 0 and lse -inf.  Keys and
+ * values beyond a request's lengths are never used, whatever they hold.
+ *   q_dev   : device bf16, token t's n_q_heads x head_dim at t * q_stride
+ *   out_dev : device bf16 at out_stride likewise; overlaps no input
+ *   lse_dev : NULL, or device fp32 [TQ][n_q_heads]
+ *   cache   : its page_size, n_kv_heads and head_dim those of the plan, its
+ *             num_pages at least the num_pages of the plan's build
+ * fp32 scores, softmax statistics and sums; the weights are rounded to bf16
+ * for the product with v.  Stream-ordered, no allocation; calls sharing a
+ * plan must not overlap in time (they share its workspace).
+ */
+lora_status lora_prefix_attention(const void *q_dev, long long q_stride, void *out_dev, long long out_stride,
+                                  float *lse_dev, const lora_kv_cache *cache, lora_attn_plan *plan, float scale,
+                                  lora_stream_t stream);
+
+/* lora_attn_plan_status: synchronise `stream` and return the plan's status
+ * word (LORA_DEV_* bits since the last build). */
+lora_status lora_attn_plan_status(const lora_attn_plan *plan, lora_stream_t stream, int *device_error);
+
+/* lora_attn_plan_destroy: synchronise the device and free the plan.  NULL is a no-op. */
+lora_status lora_attn_plan_destroy(lora_attn_plan *plan);
+
+/*
+ * lora_sample: the next token of each of T rows of logits, from one given
+ * uniform number per row.  With m the row's largest logit (NaN counts as
+ * -inf) and e_i = exp((l_i - m) / temperature), the tokens in the order of
+ * their logits (largest first, equal logits by index) are kept while they
+ * are among the first top_k, while the mass before them is below top_p times
+ * the mass of those top_k, and while e_i >= min_p; the first always is.  The
+ * token is the lowest index whose cumulative kept mass, in index order,
+ * exceeds u times the kept mass.
+ *   logits_dev : device fp32 or bf16 (logits_type LORA_TYPE_F32 / _BF16),
+ *                row t's V elements at t * row_stride elements
+ *   u_dev      : device fp32 [T] in [0, 1)
+ *   temperature_dev, top_k_dev (int32), top_p_dev, min_p_dev : device [T], or
+ *                NULL for 1, off, off, off.  temperature <= 0: the largest
+ *                logit (lowest index); top_k <= 0, top_p >= 1, min_p <= 0: off
+ *   tokens_dev : device int32 [T]; -1 for a row without a logit above -inf
+ *   probs_dev  : NULL, or device fp32 [T]: the token's share of the kept mass
+ * 1 <= V <= LORA_MAX_VOCAB, row_stride >= V.  The masses are summed in 64-bit
+ * fixed point (2^-40 of the largest token's), so the result does not depend
+ * on the order of summation.  Stream-ordered, no allocation.
+ */
+#define LORA_TYPE_F32 0
+#define LORA_TYPE_BF16 1
+#define LORA_MAX_VOCAB (1 << 20)
+lora_status lora_sample(const void *logits_dev, int logits_type, long long row_stride, int T, int V,
+                        const float *u_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                        const float *top_p_dev, const float *min_p_dev, int32_t *tokens_dev, float *probs_dev,
+                        lora_stream_t stream);
 
 #ifdef __cplusplus
 }

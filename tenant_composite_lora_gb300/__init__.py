@@ -4,8 +4,9 @@
 
 The compute lives in libtclora.so (hand-written CUDA, C ABI in
 include/lora.h).  ``native`` binds it with ctypes under the C names;
-``LoraPool`` / ``LoraMapping`` / ``delta_apply`` are small conveniences over
-torch tensors.  Importing this package does not load the library; the first
+``LoraPool`` / ``LoraMapping`` / ``delta_apply`` and, for the attention step
+around the projections, ``LoraKvCache`` / ``LoraAttnPlan`` / ``kv_append`` /
+``prefix_attention`` / ``sample`` are small conveniences over torch tensors.  Importing this package does not load the library; the first
 call does, and fails loudly if it has not been built.
 """
 from __future__ import annotations
@@ -17,7 +18,9 @@ from .native import (LoraError, lora_build_mapping, lora_delta_apply, lora_delta
                      lora_pool_create, lora_pool_destroy, lora_pool_register,
                      lora_pool_unregister, lora_version, lora_diag_wait_expiry, lora_delta_apply_multi,
                      lora_ablation_workspace_bytes, lora_delta_apply_ablation, lora_gate_logits, lora_gate_topk,
-                     lora_recompress_workspace_bytes, lora_recompress, lora_rank_allocate)
+                     lora_recompress_workspace_bytes, lora_recompress, lora_rank_allocate, lora_kv_cache_create,
+                     lora_kv_cache_destroy, lora_kv_append, lora_attn_plan_create, lora_attn_plan_build,
+                     lora_prefix_attention, lora_attn_plan_status, lora_attn_plan_destroy, lora_sample)
 
 __all__ = [
     "native", "LoraError", "LoraPool", "LoraMapping", "delta_apply",
@@ -27,7 +30,10 @@ __all__ = [
     "lora_mapping_destroy", "lora_version", "lora_delta_apply_noalloc", "lora_diag_wait_expiry",
     "lora_delta_apply_multi", "lora_ablation_workspace_bytes", "lora_delta_apply_ablation",
     "lora_gate_logits", "lora_gate_topk", "lora_recompress_workspace_bytes", "lora_recompress",
-    "lora_rank_allocate",
+    "lora_rank_allocate", "LoraKvCache", "LoraAttnPlan", "kv_append", "prefix_attention", "sample",
+    "lora_kv_cache_create", "lora_kv_cache_destroy", "lora_kv_append", "lora_attn_plan_create",
+    "lora_attn_plan_build", "lora_prefix_attention", "lora_attn_plan_status", "lora_attn_plan_destroy",
+    "lora_sample",
 ]
 
 
@@ -107,3 +113,150 @@ def delta_apply(x, y, pool: LoraPool, mapping: LoraMapping, ranks=None, path: in
         raise ValueError(f"delta_apply: ranks must hold {pool.capacity} entries, got {ranks.numel()}")
     lora_delta_apply_path(x, y, pool.handle, ranks, mapping.handle, path, stream)
     return y
+
+
+class LoraKvCache:
+    """A paged key/value cache: bf16 CUDA tensors k and v [num_pages,
+    n_kv_heads, page_size, head_dim] (allocated and zeroed unless given) and
+    their descriptor (lora_kv_cache_create / lora_kv_cache_destroy)."""
+
+    def __init__(self, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, k=None, v=None,
+                 device="cuda"):
+        import torch
+        shape = (num_pages, n_kv_heads, page_size, head_dim)
+        self.num_pages, self.page_size, self.n_kv_heads, self.head_dim = num_pages, page_size, n_kv_heads, head_dim
+        self.handle = None
+        for name, t in (("k", k), ("v", v)):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"LoraKvCache: {name} must be {shape}, got {tuple(t.shape)}")
+        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device) if k is None else k
+        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device) if v is None else v
+        self.handle = lora_kv_cache_create(num_pages, page_size, n_kv_heads, head_dim, self.k, self.v)
+
+    def close(self):
+        if self.handle:
+            lora_kv_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):  # pragma: no cover
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LoraAttnPlan:
+    """Owns an attention plan (lora_attn_plan_create / lora_attn_plan_destroy)."""
+
+    def __init__(self, max_requests: int, max_groups: int, max_queries: int, max_prefix_pages: int,
+                 max_suffix_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int):
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, n_kv_heads, head_dim, page_size
+        self.handle = None
+        self.TQ = 0
+        self.handle = lora_attn_plan_create(max_requests, max_groups, max_queries, max_prefix_pages,
+                                            max_suffix_pages, n_q_heads, n_kv_heads, head_dim, page_size)
+
+    def build(self, q_offsets, suffix_len, suffix_pages, total_queries: int, num_pages: int, group_offsets=None,
+              prefix_len=None, prefix_pages=None, stream=None):
+        """int32 CUDA tensors: q_offsets [B+1] (up to total_queries), suffix_len
+        [B], suffix_pages [B, any]; with prefixes group_offsets [NG+1],
+        prefix_len [NG], prefix_pages [NG, any].  num_pages: of the caches."""
+        if q_offsets.dim() != 1 or suffix_len.dim() != 1 or suffix_pages.dim() != 2 or q_offsets.shape[0] < 1:
+            raise ValueError("build: q_offsets and suffix_len are 1-D, suffix_pages is 2-D")
+        B = q_offsets.shape[0] - 1
+        if suffix_len.shape[0] != B or suffix_pages.shape[0] != B:
+            raise ValueError(f"build: {B} requests, but {suffix_len.shape[0]} suffix lengths and "
+                             f"{suffix_pages.shape[0]} rows of suffix pages")
+        NG = stride = 0
+        if group_offsets is not None:
+            if prefix_len is None or prefix_pages is None:
+                raise ValueError("build: group_offsets, prefix_len and prefix_pages go together")
+            if group_offsets.dim() != 1 or prefix_len.dim() != 1 or prefix_pages.dim() != 2:
+                raise ValueError("build: group_offsets and prefix_len are 1-D, prefix_pages is 2-D")
+            NG, stride = group_offsets.shape[0] - 1, prefix_pages.shape[1]
+            if NG < 0 or prefix_len.shape[0] != NG or prefix_pages.shape[0] != NG:
+                raise ValueError(f"build: {NG} groups, but {prefix_len.shape[0]} prefix lengths and "
+                                 f"{prefix_pages.shape[0]} rows of prefix pages")
+        lora_attn_plan_build(self.handle, q_offsets, suffix_len, suffix_pages, suffix_pages.shape[1],
+                             group_offsets if NG else None, prefix_len if NG else None,
+                             prefix_pages if NG else None, stride, B, NG, total_queries, num_pages, stream)
+        self.TQ = total_queries
+
+    def status(self, stream=None) -> int:
+        return lora_attn_plan_status(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            lora_attn_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):  # pragma: no cover
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def kv_append(cache: LoraKvCache, k, v, slots, positions=None, rope=None, q=None, q_out=None, interleaved=False,
+              status=None, stream=None):
+    """k, v [T, n_kv_heads, head_dim] into the cache's slots (int32 [T], -1:
+    left out), k rotated by rope [max_position, rot_dim] (float32: rot_dim / 2
+    cosines, then as many sines) at positions (int32 [T]); with q
+    [T, n_q_heads, head_dim] its rotation goes to q_out (q itself by default),
+    which is returned.  A token's heads are contiguous; tokens may be strided.
+    interleaved: pairs are neighbours instead of rot_dim / 2 apart."""
+    T, hkv, d = slots.shape[0], cache.n_kv_heads, cache.head_dim
+    kp, ks = native._rows_ptr(k, "k", T, hkv, d)
+    vp, vs = native._rows_ptr(v, "v", T, hkv, d)
+    qp = op = None
+    qs = os = hq = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        hq = q.shape[1]
+        qp, qs = native._rows_ptr(q, "q", T, hq, d)
+        op, os = native._rows_ptr(q_out, "q_out", T, hq, d)
+    rot = max_pos = 0
+    if rope is not None:
+        if rope.dim() != 2 or positions is None:
+            raise ValueError("kv_append: rope is [max_position, rot_dim] and goes with positions")
+        max_pos, rot = rope.shape
+    lora_kv_append(cache.handle, kp, ks, vp, vs, qp, qs, op, os, hq, slots, positions if rot else None,
+                   rope if rot else None, max_pos, rot,
+                   native.LORA_ROPE_ADJACENT if interleaved else native.LORA_ROPE_HALVES, T, status, stream)
+    return q_out
+
+
+def prefix_attention(q, cache: LoraKvCache, plan: LoraAttnPlan, scale=None, out=None, lse=None, stream=None):
+    """Attention of q [TQ, n_q_heads, head_dim] (bf16, tokens may be strided)
+    over the planned batch's keys; returns out (bf16, allocated unless
+    given).  lse: None or float32 [TQ, n_q_heads]; scale: 1 / sqrt(head_dim)
+    by default."""
+    T, hq, d = plan.TQ, plan.n_q_heads, plan.head_dim
+    if out is None:
+        import torch
+        out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=q.device)
+    qp, qs = native._rows_ptr(q, "q", T, hq, d)
+    op, os = native._rows_ptr(out, "out", T, hq, d)
+    if lse is not None and lse.numel() < T * hq:
+        raise ValueError(f"prefix_attention: lse must hold {T * hq} entries, got {lse.numel()}")
+    lora_prefix_attention(qp, qs, op, os, lse, cache.handle, plan.handle, d ** -0.5 if scale is None else scale,
+                          stream)
+    return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """The next token of each row of logits [T, V] (float32 or bf16 CUDA
+    tensor, rows may be strided) from u float32 [T]; temperature, top_p, min_p
+    float32 [T] and top_k int32 [T], or None.  Returns tokens (int32 [T],
+    allocated unless given); probs: None or float32 [T]."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("sample: logits are 2-D, float32 or bfloat16")
+    T, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("sample: each row of logits must be contiguous")
+    if tokens is None:
+        tokens = torch.empty(T, dtype=torch.int32, device=logits.device)
+    lora_sample(logits, native.LORA_TYPE_F32 if logits.dtype == torch.float32 else native.LORA_TYPE_BF16,
+                logits.stride(0) if T > 1 else V, T, V, u, temperature, top_k, top_p, min_p, tokens, probs, stream)
+    return tokens

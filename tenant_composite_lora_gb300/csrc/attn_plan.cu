@@ -1,0 +1,252 @@
+// The attention plan: a batch's lengths and page tables, checked and copied
+// on the device once per batch and read by every layer's attention.
+#include <cstdlib>
+
+#include "attn.h"
+#include "ptx.cuh"
+
+namespace tcl {
+
+namespace {
+
+constexpr int AP_THREADS = 1024;
+
+__device__ __forceinline__ int checked_len(int len, int pages, int page, int32_t *status)
+{
+    if (len < 0 || (long long)len > (long long)pages * page) {
+        atomicOr(status, LORA_DEV_BAD_LENGTH);
+        return 0;
+    }
+    return len;
+}
+
+// Block 0: the batch's row pointers, lengths and the request of every token;
+// the other blocks: the page tables, a warp per request or group.
+__global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, const AttnPlanSrc s)
+{
+    const int tid = threadIdx.x;
+    int32_t *status = p.hdr + AH_STATUS;
+    if (blockIdx.x == 0) {
+        int bad = 0, badg = 0;
+        for (int b = tid; b <= s.B; b += AP_THREADS) {
+            const int o = s.q_off[b];
+            bad |= (b == 0 && o != 0) || (b == s.B && o != s.TQ) || (b < s.B && s.q_off[b + 1] < o);
+        }
+        if (s.NG > 0)
+            for (int g = tid; g <= s.NG; g += AP_THREADS) {
+                const int o = s.g_off[g];
+                badg |= (g == 0 && o != 0) || (g == s.NG && o != s.B) || (g < s.NG && s.g_off[g + 1] < o);
+            }
+        bad = __syncthreads_or(bad);
+        badg = __syncthreads_or(badg);
+        const int B = bad ? 0 : s.B, NG = badg ? 0 : s.NG;
+        if (tid == 0) {
+            if (bad || badg)
+                atomicOr(status, LORA_DEV_BAD_LENGTH);
+            p.hdr[AH_NREQ] = B;
+            p.hdr[AH_NGRP] = NG;
+            p.hdr[AH_TQ] = s.TQ;
+        }
+        for (int t = tid; t < s.TQ; t += AP_THREADS) {
+            int lo = -1;
+            if (B > 0) {  // last request starting at or before t
+                lo = 0;
+                int hi = B;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s.q_off[mid] <= t)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+            }
+            p.tok_req[t] = lo;
+        }
+        for (int b = tid; b < s.B; b += AP_THREADS) {
+            p.q_off[b] = s.q_off[b];
+            p.s_len[b] = checked_len(s.s_len[b], s.s_stride, p.page, status);
+            int g = -1;
+            if (NG > 0) {
+                int hi = NG;
+                g = 0;
+                while (hi - g > 1) {
+                    const int mid = (g + hi) >> 1;
+                    if (s.g_off[mid] <= b)
+                        g = mid;
+                    else
+                        hi = mid;
+                }
+            }
+            p.grp[b] = g;
+        }
+        if (tid == 0)
+            p.q_off[s.B] = s.TQ;
+        for (int g = tid; g < s.NG; g += AP_THREADS)
+            p.p_len[g] = checked_len(s.p_len[g], s.p_stride, p.page, status);
+        return;
+    }
+    const int lane = tid & 31;
+    const int nw = (gridDim.x - 1) * (AP_THREADS / 32);
+    for (int r = (blockIdx.x - 1) * (AP_THREADS / 32) + (tid >> 5); r < s.B + s.NG; r += nw) {
+        const bool pre = r >= s.B;
+        const int i = pre ? r - s.B : r;
+        const int stride = pre ? s.p_stride : s.s_stride;
+        const int len = pre ? s.p_len[i] : s.s_len[i];
+        if (len <= 0 || (long long)len > (long long)stride * p.page)
+            continue;
+        const int n = (len + p.page - 1) / p.page;
+        const int32_t *src = (pre ? s.p_pages : s.s_pages) + (long long)i * stride;
+        int32_t *dst = pre ? p.p_pages + (long long)i * p.max_ppages : p.s_pages + (long long)i * p.max_spages;
+        for (int j = lane; j < n; j += 32) {
+            const int id = src[j];
+            const bool ok = id >= 0 && id < s.num_pages;
+            dst[j] = ok ? id : -1;
+            if (!ok)
+                atomicOr(status, LORA_DEV_BAD_PAGE);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_plan(const AttnPlanDev &p, const AttnPlanSrc &src, cudaStream_t st)
+{
+    cudaError_t e = cudaMemsetAsync(p.hdr, 0, AH_WORDS * sizeof(int32_t), st);
+    if (e != cudaSuccess)
+        return e;
+    const int rows = src.B + src.NG;
+    int blocks = (rows + AP_THREADS / 32 - 1) / (AP_THREADS / 32);
+    if (blocks > sm_count())
+        blocks = sm_count();
+    k_attn_plan<<<1 + blocks, AP_THREADS, 0, st>>>(p, src);
+    return cudaGetLastError();
+}
+
+namespace {
+
+template <typename T>
+cudaError_t plan_alloc(T **p, size_t n)
+{
+    return cudaMalloc(reinterpret_cast<void **>(p), (n ? n : 1) * sizeof(T));
+}
+
+void free_plan(lora_attn_plan *p)
+{
+    if (!p)
+        return;
+    AttnPlanDev &d = p->dev;
+    void *all[] = {d.hdr, d.q_off, d.s_len, d.grp, d.p_len, d.tok_req, d.s_pages, d.p_pages};
+    for (void *x : all)
+        if (x)
+            cudaFree(x);
+    std::free(p);
+}
+
+lora_status status_of(cudaError_t e)
+{
+    return e == cudaSuccess ? LORA_OK : e == cudaErrorMemoryAllocation ? LORA_ERR_OUT_OF_MEMORY : LORA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" {
+
+lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_queries, int max_prefix_pages,
+                                  int max_suffix_pages, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                  lora_attn_plan **out)
+{
+    if (!out)
+        return LORA_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (max_requests < 1 || max_groups < 0 || max_queries < 1 || max_prefix_pages < 0 || max_suffix_pages < 0 ||
+        n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || head_dim < 1 || page_size < 1)
+        return LORA_ERR_INVALID_ARG;
+    if ((page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+        (head_dim != 64 && head_dim != 128) || n_kv_heads > LORA_MAX_KV_HEADS || n_q_heads > LORA_MAX_Q_HEADS ||
+        max_requests > LORA_MAX_TOKENS || max_groups > LORA_MAX_TOKENS || max_queries > LORA_MAX_TOKENS ||
+        max_prefix_pages > (1 << 24) || max_suffix_pages > (1 << 24))
+        return LORA_ERR_NOT_SUPPORTED;
+    lora_attn_plan *p = static_cast<lora_attn_plan *>(std::calloc(1, sizeof(lora_attn_plan)));
+    if (!p)
+        return LORA_ERR_OUT_OF_MEMORY;
+    p->max_requests = max_requests;
+    p->max_groups = max_groups;
+    p->max_queries = max_queries;
+    cudaGetDevice(&p->device);
+    AttnPlanDev &d = p->dev;
+    d.max_spages = max_suffix_pages;
+    d.max_ppages = max_prefix_pages;
+    d.hq = n_q_heads;
+    d.hkv = n_kv_heads;
+    d.d = head_dim;
+    d.page = page_size;
+    d.page_log2 = __builtin_ctz((unsigned)page_size);
+    cudaError_t e = plan_alloc(&d.hdr, AH_WORDS);
+    if (e == cudaSuccess) e = plan_alloc(&d.q_off, (size_t)max_requests + 1);
+    if (e == cudaSuccess) e = plan_alloc(&d.s_len, (size_t)max_requests);
+    if (e == cudaSuccess) e = plan_alloc(&d.grp, (size_t)max_requests);
+    if (e == cudaSuccess) e = plan_alloc(&d.p_len, (size_t)max_groups);
+    if (e == cudaSuccess) e = plan_alloc(&d.tok_req, (size_t)max_queries);
+    if (e == cudaSuccess) e = plan_alloc(&d.s_pages, (size_t)max_requests * max_suffix_pages);
+    if (e == cudaSuccess) e = plan_alloc(&d.p_pages, (size_t)max_groups * max_prefix_pages);
+    if (e == cudaSuccess) e = cudaMemset(d.hdr, 0, AH_WORDS * sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        free_plan(p);
+        return status_of(e);
+    }
+    *out = p;
+    return LORA_OK;
+}
+
+lora_status lora_attn_plan_build(lora_attn_plan *plan, const int32_t *q_offsets_dev, const int32_t *suffix_len_dev,
+                                 const int32_t *suffix_pages_dev, int suffix_stride, const int32_t *group_offsets_dev,
+                                 const int32_t *prefix_len_dev, const int32_t *prefix_pages_dev, int prefix_stride,
+                                 int B, int NG, int TQ, int num_pages, lora_stream_t stream)
+{
+    if (!plan || !q_offsets_dev || B < 0 || NG < 0 || TQ < 0 || num_pages < 1 || suffix_stride < 0 ||
+        prefix_stride < 0 || B > plan->max_requests || NG > plan->max_groups || TQ > plan->max_queries ||
+        suffix_stride > plan->dev.max_spages || (NG > 0 && prefix_stride > plan->dev.max_ppages))
+        return LORA_ERR_INVALID_ARG;
+    if ((B > 0 && (!suffix_len_dev || (suffix_stride > 0 && !suffix_pages_dev))) ||
+        (NG > 0 && (!group_offsets_dev || !prefix_len_dev || (prefix_stride > 0 && !prefix_pages_dev))))
+        return LORA_ERR_INVALID_ARG;
+    const AttnPlanSrc src{q_offsets_dev, suffix_len_dev, suffix_pages_dev, group_offsets_dev, prefix_len_dev,
+                          prefix_pages_dev, suffix_stride, prefix_stride, B, NG, TQ, num_pages};
+    const cudaError_t e = launch_attn_plan(plan->dev, src, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return status_of(e);
+    plan->TQ = TQ;
+    plan->num_pages = num_pages;
+    plan->built = true;
+    return LORA_OK;
+}
+
+lora_status lora_attn_plan_status(const lora_attn_plan *plan, lora_stream_t stream, int *device_error)
+{
+    if (!plan || !device_error)
+        return LORA_ERR_INVALID_ARG;
+    int32_t v = 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&v, plan->dev.hdr + AH_STATUS, sizeof(int32_t), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    *device_error = v;
+    return status_of(e);
+}
+
+lora_status lora_attn_plan_destroy(lora_attn_plan *plan)
+{
+    if (!plan)
+        return LORA_OK;
+    const cudaError_t e = cudaDeviceSynchronize();
+    free_plan(plan);
+    return status_of(e);
+}
+
+}  // extern "C"

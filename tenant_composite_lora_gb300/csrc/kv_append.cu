@@ -1,0 +1,231 @@
+// The paged key/value cache and the append of a batch's tokens to it, keys
+// and queries rotated by their positions on the way (lora_kv_append).
+//
+// A rotation mixes the pairs (a, b) of a head's first rot_dim elements:
+//     a' = a c - b s,  b' = b c + a s,   c, s = rope[position][i], rope[position][rot_dim / 2 + i],
+// in fp32, rounded once to bf16.  Pure movement: every element is read and
+// written once.
+#include <cstdlib>
+
+#include "attn.h"
+#include "ptx.cuh"
+
+namespace tcl {
+
+namespace {
+
+struct AppendArgs {
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16 *kc, *vc, *qo;
+    long long ks, vs, qs, os;
+    const int32_t *slots, *pos;
+    const float *rope;
+    int32_t *status;
+    int max_pos, rot, T, hq, hkv, d, page, page_log2;
+    long long cap;  // slots of the cache
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A thread moves two 16-byte chunks of one head of one token: with halves
+// style in the rotated part a chunk and the one rot / 2 elements on.
+template <bool HALVES>
+__global__ void __launch_bounds__(256) k_kv_append(const AppendArgs a)
+{
+    const int upr = a.d / 16;                   // units (chunk pairs) per head
+    const int heads = a.hq + 2 * a.hkv;         // q heads, then k heads, then v heads
+    const long long n = (long long)a.T * heads * upr;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n)
+        return;
+    const int u = (int)(i % upr);
+    const long long row = i / upr;
+    const int h = (int)(row % heads), t = (int)(row / heads);
+
+    int pos = 0;
+    if (a.rot > 0) {
+        pos = a.pos[t];
+        if (pos < 0 || pos >= a.max_pos) {
+            if (h == 0 && u == 0 && a.status)
+                atomicOr(a.status, LORA_DEV_BAD_POSITION);
+            return;
+        }
+    }
+    const __nv_bfloat16 *src;
+    __nv_bfloat16 *dst;
+    bool rotate = a.rot > 0;
+    if (h < a.hq) {
+        src = a.q + t * a.qs + (long long)h * a.d;
+        dst = a.qo + t * a.os + (long long)h * a.d;
+    } else {
+        const int slot = a.slots[t];
+        if (slot < 0 || slot >= a.cap) {
+            if (slot != -1 && h == a.hq && u == 0 && a.status)
+                atomicOr(a.status, LORA_DEV_BAD_SLOT);
+            return;
+        }
+        const bool is_v = h >= a.hq + a.hkv;
+        const int hh = h - a.hq - (is_v ? a.hkv : 0);
+        src = (is_v ? a.v + t * a.vs : a.k + t * a.ks) + (long long)hh * a.d;
+        const long long pg = slot >> a.page_log2;
+        dst = (is_v ? a.vc : a.kc) + ((pg * a.hkv + hh) * a.page + (slot & (a.page - 1))) * a.d;
+        rotate = rotate && !is_v;
+    }
+    // chunk indices of the pair of chunks
+    int c0, c1;
+    const int hr = a.rot / 16;  // chunks of half the rotated part
+    if (HALVES && u < hr) {
+        c0 = u;
+        c1 = u + hr;
+    } else {
+        c0 = 2 * u;
+        c1 = 2 * u + 1;
+    }
+    uint4 x = *reinterpret_cast<const uint4 *>(src + c0 * 8);
+    uint4 y = *reinterpret_cast<const uint4 *>(src + c1 * 8);
+    if (rotate && u < hr) {
+        const float *row_p = a.rope + (long long)pos * a.rot;
+        if (HALVES) {
+            const float *cp = row_p + c0 * 8, *sp = cp + a.rot / 2;
+            uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 c = *reinterpret_cast<const float2 *>(cp + 2 * j);
+                const float2 s = *reinterpret_cast<const float2 *>(sp + 2 * j);
+                const float a0 = bf16lo(xs[j]), a1 = bf16hi(xs[j]), b0 = bf16lo(ys[j]), b1 = bf16hi(ys[j]);
+                xs[j] = pack2(a0 * c.x - b0 * s.x, a1 * c.y - b1 * s.y);
+                ys[j] = pack2(b0 * c.x + a0 * s.x, b1 * c.y + a1 * s.y);
+            }
+            x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+            y = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+        } else {
+            // 16 consecutive elements: 8 adjacent pairs, tables from pair 8 u
+            const float *cp = row_p + u * 8, *sp = cp + a.rot / 2;
+            uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float c = cp[j], s = sp[j], e = bf16lo(w[j]), o = bf16hi(w[j]);
+                w[j] = pack2(e * c - o * s, o * c + e * s);
+            }
+            x = make_uint4(w[0], w[1], w[2], w[3]);
+            y = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+    *reinterpret_cast<uint4 *>(dst + c0 * 8) = x;
+    *reinterpret_cast<uint4 *>(dst + c1 * 8) = y;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" {
+
+lora_status lora_kv_cache_create(int num_pages, int page_size, int n_kv_heads, int head_dim, void *k_dev, void *v_dev,
+                                 lora_kv_cache **out)
+{
+    if (!out)
+        return LORA_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (num_pages < 1 || page_size < 1 || n_kv_heads < 1 || head_dim < 1 || !k_dev || !v_dev || !aligned16(k_dev) ||
+        !aligned16(v_dev))
+        return LORA_ERR_INVALID_ARG;
+    if ((page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+        (head_dim != 64 && head_dim != 128) || n_kv_heads > LORA_MAX_KV_HEADS ||
+        (long long)num_pages * n_kv_heads * page_size >= (1ll << 31))
+        return LORA_ERR_NOT_SUPPORTED;
+    lora_kv_cache *c = static_cast<lora_kv_cache *>(std::calloc(1, sizeof(lora_kv_cache)));
+    if (!c)
+        return LORA_ERR_OUT_OF_MEMORY;
+    c->num_pages = num_pages;
+    c->page_size = page_size;
+    c->hkv = n_kv_heads;
+    c->d = head_dim;
+    c->k = static_cast<__nv_bfloat16 *>(k_dev);
+    c->v = static_cast<__nv_bfloat16 *>(v_dev);
+    *out = c;
+    return LORA_OK;
+}
+
+lora_status lora_kv_cache_destroy(lora_kv_cache *cache)
+{
+    std::free(cache);
+    return LORA_OK;
+}
+
+lora_status lora_kv_append(const lora_kv_cache *cache, const void *k_dev, long long k_stride, const void *v_dev,
+                           long long v_stride, const void *q_dev, long long q_stride, void *q_out_dev,
+                           long long out_stride, int n_q_heads, const int32_t *slots_dev, const int32_t *positions_dev,
+                           const float *rope_dev, int max_position, int rot_dim, int style, int T,
+                           int32_t *status_dev, lora_stream_t stream)
+{
+    if (!cache || T < 0 || rot_dim < 0 || rot_dim > cache->d || rot_dim % 16 ||
+        (style != LORA_ROPE_HALVES && style != LORA_ROPE_ADJACENT))
+        return LORA_ERR_INVALID_ARG;
+    if (T > LORA_MAX_TOKENS)
+        return LORA_ERR_NOT_SUPPORTED;
+    if (T == 0)
+        return LORA_OK;  // (arrays of no elements may have no address)
+    if (!k_dev || !v_dev || !slots_dev)
+        return LORA_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!positions_dev || !rope_dev || max_position < 1 || !aligned16(rope_dev)))
+        return LORA_ERR_INVALID_ARG;
+    const long long kv_row = (long long)cache->hkv * cache->d;
+    if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8 || !aligned16(k_dev) ||
+        !aligned16(v_dev))
+        return LORA_ERR_INVALID_ARG;
+    if (q_dev) {
+        if (!q_out_dev || n_q_heads < 1 || !aligned16(q_dev) || !aligned16(q_out_dev) || q_stride % 8 ||
+            out_stride % 8)
+            return LORA_ERR_INVALID_ARG;
+        if (n_q_heads > LORA_MAX_Q_HEADS)
+            return LORA_ERR_NOT_SUPPORTED;
+        const long long q_row = (long long)n_q_heads * cache->d;
+        if (q_stride < q_row || out_stride < q_row || (q_dev == q_out_dev && q_stride != out_stride))
+            return LORA_ERR_INVALID_ARG;
+    }
+    AppendArgs a{};
+    a.k = static_cast<const __nv_bfloat16 *>(k_dev);
+    a.v = static_cast<const __nv_bfloat16 *>(v_dev);
+    a.q = static_cast<const __nv_bfloat16 *>(q_dev);
+    a.kc = cache->k;
+    a.vc = cache->v;
+    a.qo = static_cast<__nv_bfloat16 *>(q_out_dev);
+    a.ks = k_stride;
+    a.vs = v_stride;
+    a.qs = q_stride;
+    a.os = out_stride;
+    a.slots = slots_dev;
+    a.pos = positions_dev;
+    a.rope = rope_dev;
+    a.status = status_dev;
+    a.max_pos = max_position;
+    a.rot = rot_dim;
+    a.T = T;
+    a.hq = q_dev ? n_q_heads : 0;
+    a.hkv = cache->hkv;
+    a.d = cache->d;
+    a.page = cache->page_size;
+    a.page_log2 = __builtin_ctz((unsigned)cache->page_size);
+    a.cap = (long long)cache->num_pages * cache->page_size;
+    const long long n = (long long)T * (a.hq + 2 * a.hkv) * (a.d / 16);
+    const long long grid = (n + 255) / 256;
+    if (grid > 0x7fffffffll)
+        return LORA_ERR_NOT_SUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (style == LORA_ROPE_HALVES)
+        k_kv_append<true><<<(unsigned)grid, 256, 0, st>>>(a);
+    else
+        k_kv_append<false><<<(unsigned)grid, 256, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+}  // extern "C"

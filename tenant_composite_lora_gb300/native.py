@@ -30,6 +30,10 @@ LORA_DEV_BAD_OFFSETS = 2
 LORA_DEV_UNREGISTERED = 4
 LORA_DEV_BAD_RANK = 8
 LORA_DEV_TIMEOUT = 16
+LORA_DEV_BAD_SLOT = 32
+LORA_DEV_BAD_POSITION = 64
+LORA_DEV_BAD_PAGE = 128
+LORA_DEV_BAD_LENGTH = 256
 
 LORA_PATH_AUTO = 0
 LORA_PATH_SPLIT = 1
@@ -48,7 +52,9 @@ EXPORTS = [
     "lora_mapping_destroy", "lora_status_string", "lora_version", "lora_delta_apply_noalloc",
     "lora_diag_wait_expiry", "lora_delta_apply_multi", "lora_ablation_workspace_bytes",
     "lora_delta_apply_ablation", "lora_gate_logits", "lora_gate_topk", "lora_recompress_workspace_bytes",
-    "lora_recompress", "lora_rank_allocate",
+    "lora_recompress", "lora_rank_allocate", "lora_kv_cache_create", "lora_kv_cache_destroy", "lora_kv_append",
+    "lora_attn_plan_create", "lora_attn_plan_build", "lora_prefix_attention", "lora_attn_plan_status",
+    "lora_attn_plan_destroy", "lora_sample",
 ]
 
 LORA_RANK_UNIFORM = 0
@@ -59,6 +65,13 @@ LORA_ABLATION_COPY_SGMV = 2
 LORA_ABLATION_PREMERGE = 3
 
 LORA_MAX_PROJECTIONS = 8
+
+LORA_ROPE_HALVES = 0
+LORA_ROPE_ADJACENT = 1
+
+LORA_TYPE_F32 = 0
+LORA_TYPE_BF16 = 1
+LORA_MAX_VOCAB = 1 << 20
 
 
 class LoraProjection(ctypes.Structure):
@@ -91,6 +104,7 @@ def load(path: str | None = None):
             "(there is no CPU or Python fallback)")
     lib = ctypes.CDLL(path)
     V, I, PP = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)
+    L = ctypes.c_longlong
     sig = {
         "lora_pool_create": ([I, I, I, I, PP], I),
         "lora_pool_register": ([V, I, V, V, I, V], I),
@@ -117,6 +131,15 @@ def load(path: str | None = None):
         "lora_recompress_workspace_bytes": ([I, I, I], ctypes.c_size_t),
         "lora_recompress": ([V, V, I, I, I, I, V, V, V, V, ctypes.c_size_t, V], I),
         "lora_rank_allocate": ([V, I, I, V, V, I, I, I, V], I),
+        "lora_kv_cache_create": ([I, I, I, I, V, V, PP], I),
+        "lora_kv_cache_destroy": ([V], I),
+        "lora_kv_append": ([V, V, L, V, L, V, L, V, L, I, V, V, V, I, I, I, I, V, V], I),
+        "lora_attn_plan_create": ([I, I, I, I, I, I, I, I, I, PP], I),
+        "lora_attn_plan_build": ([V, V, V, V, I, V, V, V, I, I, I, I, I, V], I),
+        "lora_prefix_attention": ([V, L, V, L, V, V, V, ctypes.c_float, V], I),
+        "lora_attn_plan_status": ([V, V, ctypes.POINTER(ctypes.c_int)], I),
+        "lora_attn_plan_destroy": ([V], I),
+        "lora_sample": ([V, I, L, I, I, V, V, V, V, V, V, V, V], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -474,6 +497,127 @@ def lora_diag_wait_expiry(kind: int, limit_ns: int, words, stream=None):
     _need("lora_diag_wait_expiry", "words", words, 4)
     _check("lora_diag_wait_expiry",
            load().lora_diag_wait_expiry(kind, limit_ns, _dptr(words, "words", "int32"), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the attention step
+def _rows_ptr(t, name: str, T: int, heads: int, d: int):
+    """(address, elements between tokens) of a [T, heads, d] bf16 CUDA tensor
+    whose heads are contiguous: a slice of a fused projection's output goes
+    in as it is."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is expected, got one on {t.device}")
+    if not _dtype_ok(t, "bf16"):
+        raise ValueError(f"{name}: bf16 elements expected, got {t.dtype}")
+    if tuple(t.shape) != (T, heads, d):
+        raise ValueError(f"{name}: shape {(T, heads, d)} expected, got {tuple(t.shape)}")
+    st = t.stride()
+    if T and (st[2] != 1 or (heads > 1 and st[1] != d)):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else heads * d
+
+
+def lora_kv_cache_create(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, k, v) -> int:
+    """k, v: bf16 CUDA tensors [num_pages, n_kv_heads, page_size, head_dim]
+    (or raw addresses), which the caller keeps alive."""
+    if num_pages > 0 and page_size > 0 and n_kv_heads > 0 and head_dim > 0:
+        n = num_pages * page_size * n_kv_heads * head_dim
+        _need("lora_kv_cache_create", "k", k, n)
+        _need("lora_kv_cache_create", "v", v, n)
+    out = ctypes.c_void_p()
+    _check("lora_kv_cache_create",
+           load().lora_kv_cache_create(num_pages, page_size, n_kv_heads, head_dim, _dptr(k, "k", "bf16"),
+                                       _dptr(v, "v", "bf16"), ctypes.byref(out)))
+    return out.value
+
+
+def lora_kv_cache_destroy(cache: int):
+    _check("lora_kv_cache_destroy", load().lora_kv_cache_destroy(cache))
+
+
+def lora_kv_append(cache: int, k, k_stride: int, v, v_stride: int, q, q_stride: int, q_out, out_stride: int,
+                   n_q_heads: int, slots, positions, rope, max_position: int, rot_dim: int, style: int, T: int,
+                   status=None, stream=None):
+    """k, v, q, q_out: addresses (see ``_rows_ptr``); the other arrays as
+    tensors or addresses."""
+    fn = "lora_kv_append"
+    _need(fn, "slots", slots, T)
+    if rot_dim > 0:
+        _need(fn, "positions", positions, T)
+        _need(fn, "rope", rope, max_position * rot_dim)
+    _check(fn, load().lora_kv_append(cache, k, k_stride, v, v_stride, q, q_stride, q_out, out_stride, n_q_heads,
+                                     _dptr(slots, "slots", "int32"), _dptr(positions, "positions", "int32"),
+                                     _dptr(rope, "rope", "float32"), max_position, rot_dim, style, T,
+                                     _dptr(status, "status", "int32"), _stream(stream)))
+
+
+def lora_attn_plan_create(max_requests: int, max_groups: int, max_queries: int, max_prefix_pages: int,
+                          max_suffix_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                          page_size: int) -> int:
+    out = ctypes.c_void_p()
+    _check("lora_attn_plan_create",
+           load().lora_attn_plan_create(max_requests, max_groups, max_queries, max_prefix_pages, max_suffix_pages,
+                                        n_q_heads, n_kv_heads, head_dim, page_size, ctypes.byref(out)))
+    return out.value
+
+
+def lora_attn_plan_build(plan: int, q_offsets, suffix_len, suffix_pages, suffix_stride: int, group_offsets,
+                         prefix_len, prefix_pages, prefix_stride: int, B: int, NG: int, TQ: int, num_pages: int,
+                         stream=None):
+    fn = "lora_attn_plan_build"
+    _need(fn, "q_offsets", q_offsets, B + 1)
+    _need(fn, "suffix_len", suffix_len, B)
+    _need(fn, "suffix_pages", suffix_pages, B * suffix_stride)
+    if NG > 0:
+        _need(fn, "group_offsets", group_offsets, NG + 1)
+        _need(fn, "prefix_len", prefix_len, NG)
+        _need(fn, "prefix_pages", prefix_pages, NG * prefix_stride)
+    i32 = "int32"
+    _check(fn, load().lora_attn_plan_build(plan, _dptr(q_offsets, "q_offsets", i32),
+                                           _dptr(suffix_len, "suffix_len", i32),
+                                           _dptr(suffix_pages, "suffix_pages", i32), suffix_stride,
+                                           _dptr(group_offsets, "group_offsets", i32),
+                                           _dptr(prefix_len, "prefix_len", i32),
+                                           _dptr(prefix_pages, "prefix_pages", i32), prefix_stride, B, NG, TQ,
+                                           num_pages, _stream(stream)))
+
+
+def lora_prefix_attention(q, q_stride: int, out, out_stride: int, lse, cache: int, plan: int, scale: float,
+                          stream=None):
+    """q, out: addresses (see ``_rows_ptr``)."""
+    _check("lora_prefix_attention",
+           load().lora_prefix_attention(q, q_stride, out, out_stride, _dptr(lse, "lse", "float32"), cache, plan,
+                                        scale, _stream(stream)))
+
+
+def lora_attn_plan_status(plan: int, stream=None) -> int:
+    v = ctypes.c_int()
+    _check("lora_attn_plan_status", load().lora_attn_plan_status(plan, _stream(stream), ctypes.byref(v)))
+    return int(v.value)
+
+
+def lora_attn_plan_destroy(plan: int):
+    _check("lora_attn_plan_destroy", load().lora_attn_plan_destroy(plan))
+
+
+def lora_sample(logits, logits_type: int, row_stride: int, T: int, V: int, u, temperature, top_k, top_p, min_p, tokens,
+                probs=None, stream=None):
+    """logits: an address, or a tensor of T rows of V elements row_stride
+    apart whose type is logits_type's."""
+    fn = "lora_sample"
+    if logits is not None and not isinstance(logits, int):
+        if not logits.is_cuda:
+            raise ValueError(f"logits: a CUDA tensor is expected, got one on {logits.device}")
+        if logits.element_size() != (4 if logits_type == LORA_TYPE_F32 else 2):
+            raise ValueError(f"logits: elements of logits_type {logits_type} expected, got {logits.dtype}")
+        logits = logits.data_ptr()
+    for name, t in (("u", u), ("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p),
+                    ("tokens", tokens), ("probs", probs)):
+        _need(fn, name, t, T)
+    f32 = "float32"
+    _check(fn, load().lora_sample(logits, logits_type, row_stride, T, V, _dptr(u, "u", f32),
+                                  _dptr(temperature, "temperature", f32), _dptr(top_k, "top_k", "int32"),
+                                  _dptr(top_p, "top_p", f32), _dptr(min_p, "min_p", f32),
+                                  _dptr(tokens, "tokens", "int32"), _dptr(probs, "probs", f32), _stream(stream)))
 
 
 def lora_version() -> str:
