@@ -20,10 +20,71 @@ __device__ __forceinline__ int checked_len(int len, int pages, int page, int32_t
     return len;
 }
 
-// Block 0: the batch's row pointers, lengths and the request of every token;
-// the other blocks: the page tables, a warp per request or group.
+// Sums of a thread's value over the threads before it, and over all.
+__device__ long long block_before(long long v, long long &total, long long *sh /* [33] */)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o)
+            inc += x;
+    }
+    if (lane == 31)
+        sh[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        long long w = sh[lane], s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                s += x;
+        }
+        sh[lane] = s - w;
+        if (lane == 31)
+            sh[32] = s;
+    }
+    __syncthreads();
+    const long long r = sh[warp] + inc - v;
+    total = sh[32];
+    __syncthreads();
+    return r;
+}
+
+// Last entry of the ascending row pointer off[0 .. n] at or below x, as an index below n.
+template <typename T>
+__device__ __forceinline__ int row_of(const T *off, int n, T x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// What a group (i < NG) or request reads: its query tokens, its keys.
+struct Reader {
+    int t0, n, len, lim;
+};
+
+// Keys that the last row of row tile k sees.
+__device__ __forceinline__ int tile_keys(const Reader &r, int G, int k)
+{
+    const int last = min(r.n * G, (k + 1) * NA_ROWS) - 1;
+    return max(0, min(r.len, r.t0 + last / G + r.lim));
+}
+
+// Block 0: the batch's row pointers and lengths, the segments and the CTAs'
+// runs; the other blocks: the page tables, a warp per request or group.
 __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, const AttnPlanSrc s)
 {
+    __shared__ long long sh[33];
     const int tid = threadIdx.x;
     int32_t *status = p.hdr + AH_STATUS;
     if (blockIdx.x == 0) {
@@ -39,50 +100,87 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
             }
         bad = __syncthreads_or(bad);
         badg = __syncthreads_or(badg);
-        const int B = bad ? 0 : s.B, NG = badg ? 0 : s.NG;
+        const int B = bad ? 0 : s.B, NG = bad || badg ? 0 : s.NG;
         if (tid == 0) {
             if (bad || badg)
                 atomicOr(status, LORA_DEV_BAD_LENGTH);
             p.hdr[AH_NREQ] = B;
             p.hdr[AH_NGRP] = NG;
-            p.hdr[AH_TQ] = s.TQ;
         }
-        for (int t = tid; t < s.TQ; t += AP_THREADS) {
-            int lo = -1;
-            if (B > 0) {  // last request starting at or before t
-                lo = 0;
-                int hi = B;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s.q_off[mid] <= t)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
-            }
-            p.tok_req[t] = lo;
-        }
-        for (int b = tid; b < s.B; b += AP_THREADS) {
+        for (int t = tid; t < s.TQ; t += AP_THREADS)
+            p.tok_req[t] = B > 0 ? row_of(s.q_off, B, t) : -1;
+        for (int b = tid; b < B; b += AP_THREADS) {
             p.q_off[b] = s.q_off[b];
-            p.s_len[b] = checked_len(s.s_len[b], s.s_stride, p.page, status);
-            int g = -1;
-            if (NG > 0) {
-                int hi = NG;
-                g = 0;
-                while (hi - g > 1) {
-                    const int mid = (g + hi) >> 1;
-                    if (s.g_off[mid] <= b)
-                        g = mid;
-                    else
-                        hi = mid;
-                }
-            }
-            p.grp[b] = g;
+            p.grp[b] = NG > 0 ? row_of(s.g_off, NG, b) : -1;
         }
-        if (tid == 0)
-            p.q_off[s.B] = s.TQ;
-        for (int g = tid; g < s.NG; g += AP_THREADS)
-            p.p_len[g] = checked_len(s.p_len[g], s.p_stride, p.page, status);
+        // the segments: groups, then requests
+        const int G = p.hq / p.hkv;
+        long long segs = 0, tiles = 0, rows = 0;
+        for (int i0 = 0; i0 < NG + B; i0 += AP_THREADS) {
+            const int i = i0 + tid;
+            Reader r{0, 0, 0, 0};
+            if (i < NG) {
+                r.t0 = s.q_off[s.g_off[i]];
+                r.n = s.q_off[s.g_off[i + 1]] - r.t0;
+                r.len = checked_len(s.p_len[i], s.p_stride, p.page, status);
+                r.lim = 1 << 30;
+                p.g_row0[i] = r.t0;
+            } else if (i < NG + B) {
+                const int b = i - NG;
+                r.t0 = s.q_off[b];
+                r.n = s.q_off[b + 1] - r.t0;
+                r.len = checked_len(s.s_len[b], s.s_stride, p.page, status);
+                r.lim = r.len - r.n + 1 - r.t0;
+            }
+            const int nt = r.len > 0 ? (int)(((long long)r.n * G + NA_ROWS - 1) / NA_ROWS) : 0;
+            long long my_tiles = 0;
+            for (int k = 0; k < nt; ++k)
+                my_tiles += (tile_keys(r, G, k) + NA_KEYS - 1) / NA_KEYS;
+            long long all;
+            long long seg0 = segs + block_before(nt, all, sh);
+            segs += all;
+            long long a = tiles + p.hkv * block_before(my_tiles, all, sh);
+            tiles += p.hkv * all;
+            long long row = rows + p.hkv * block_before(nt > 0 ? (long long)r.n * G : 0, all, sh);
+            rows += p.hkv * all;
+            if (i < NG)
+                p.pseg[i] = nt > 0 ? (int)seg0 : -1;
+            else if (i < NG + B)
+                p.sseg[i - NG] = nt > 0 ? (int)seg0 : -1;
+            for (int k = 0; k < nt; ++k) {
+                AttnSeg g;
+                g.a = a;
+                g.rows0 = row;
+                g.row0 = r.t0 * G + k * NA_ROWS;
+                g.nrows = min(NA_ROWS, r.n * G - k * NA_ROWS);
+                g.nkeys = tile_keys(r, G, k);
+                g.ntiles = (g.nkeys + NA_KEYS - 1) / NA_KEYS;
+                g.src = i < NG ? ~i : i - NG;
+                g.lim = r.lim;
+                p.seg[seg0 + k] = g;
+                a += (long long)p.hkv * g.ntiles;
+                row += (long long)p.hkv * g.nrows;
+            }
+        }
+        const long long run = (tiles + p.ctas - 1) / p.ctas;
+        if (tid == 0) {
+            p.hdr[AH_NSEG] = (int)segs;
+            p.len[AL_TILES] = tiles;
+            p.len[AL_RUN] = run;
+        }
+        __syncthreads();  // the segments are written (by this block)
+        for (int c = tid; c < p.ctas; c += AP_THREADS) {
+            const long long at = c * run;
+            int lo = 0, hi = (int)segs;  // last segment starting at or before `at`: the one that holds it
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.seg[mid].a <= at)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            p.cta_seg[c] = lo;
+        }
         return;
     }
     const int lane = tid & 31;
@@ -135,7 +233,8 @@ void free_plan(lora_attn_plan *p)
     if (!p)
         return;
     AttnPlanDev &d = p->dev;
-    void *all[] = {d.hdr, d.q_off, d.s_len, d.grp, d.p_len, d.tok_req, d.s_pages, d.p_pages};
+    void *all[] = {d.hdr,  d.len,     d.q_off,   d.grp, d.g_row0,  d.tok_req, d.sseg,
+                   d.pseg, d.s_pages, d.p_pages, d.seg, d.cta_seg, d.part,    d.part_ml};
     for (void *x : all)
         if (x)
             cudaFree(x);
@@ -185,14 +284,32 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     d.d = head_dim;
     d.page = page_size;
     d.page_log2 = __builtin_ctz((unsigned)page_size);
+    d.ctas = NA_CTAS_PER_SM * sm_count();
+    // a row tile of every group and request and one per full tile of rows;
+    // a query row has partial rows for the prefix and the request's own
+    // tokens, and each end of a CTA's run splits one row tile
+    const long long tokens_rows = (long long)max_queries * (n_q_heads / n_kv_heads);
+    const long long segs = (long long)max_groups + max_requests + 2 * (tokens_rows / NA_ROWS + 1);
+    const long long part_rows = (long long)d.ctas * NA_ROWS + 2ll * max_queries * n_q_heads;
+    if (segs > 0x7fffffffll || tokens_rows > 0x3fffffffll) {
+        free_plan(p);
+        return LORA_ERR_NOT_SUPPORTED;
+    }
+    d.max_segs = (int)segs;
     cudaError_t e = plan_alloc(&d.hdr, AH_WORDS);
     if (e == cudaSuccess) e = plan_alloc(&d.q_off, (size_t)max_requests + 1);
-    if (e == cudaSuccess) e = plan_alloc(&d.s_len, (size_t)max_requests);
+    if (e == cudaSuccess) e = plan_alloc(&d.len, AL_WORDS);
     if (e == cudaSuccess) e = plan_alloc(&d.grp, (size_t)max_requests);
-    if (e == cudaSuccess) e = plan_alloc(&d.p_len, (size_t)max_groups);
+    if (e == cudaSuccess) e = plan_alloc(&d.g_row0, (size_t)max_groups);
+    if (e == cudaSuccess) e = plan_alloc(&d.sseg, (size_t)max_requests);
+    if (e == cudaSuccess) e = plan_alloc(&d.pseg, (size_t)max_groups);
     if (e == cudaSuccess) e = plan_alloc(&d.tok_req, (size_t)max_queries);
     if (e == cudaSuccess) e = plan_alloc(&d.s_pages, (size_t)max_requests * max_suffix_pages);
     if (e == cudaSuccess) e = plan_alloc(&d.p_pages, (size_t)max_groups * max_prefix_pages);
+    if (e == cudaSuccess) e = plan_alloc(&d.seg, (size_t)segs);
+    if (e == cudaSuccess) e = plan_alloc(&d.cta_seg, (size_t)d.ctas);
+    if (e == cudaSuccess) e = plan_alloc(&d.part, (size_t)part_rows * head_dim);
+    if (e == cudaSuccess) e = plan_alloc(&d.part_ml, (size_t)part_rows);
     if (e == cudaSuccess) e = cudaMemset(d.hdr, 0, AH_WORDS * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {

@@ -956,15 +956,15 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// Row-major bf16 matrix [rows][cols], boxes of 16 rows x 64 columns, 128-byte swizzle.
-cudaError_t encode_rows(unsigned char *out, const void *base, int cols, long long rows)
+// Row-major bf16 matrix [rows][cols], boxes of box_rows rows x 64 columns, 128-byte swizzle.
+cudaError_t encode_rows(unsigned char *out, const void *base, int cols, long long rows, int box_rows = 16)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn)
         return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {64, 16};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = fn(reinterpret_cast<CUtensorMap *>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1041,6 +1041,11 @@ cudaError_t launch_expand_bn(__nv_bfloat16 *y, const PoolDev &pool, const CUtens
 }
 
 }  // namespace
+
+cudaError_t encode_kv_rows(unsigned char *map, const void *base, int d, long long rows, int box_rows)
+{
+    return encode_rows(map, base, d, rows, box_rows);
+}
 
 bool mma_supported(int d_in, int d_out, int r_max)
 {
