@@ -15,25 +15,18 @@
 //    them; their sums are joined at a piece's end.  Bound by the cache's
 //    bytes: a tile of 16 KB of keys and as much of values costs each warp 16
 //    + 32 small products.
+//  * k_attn_wide (attn_wide.cu): tiles of 256 rows and 128 keys on the tensor
+//    memory's matrix instructions, for prefixes of many requests and for
+//    prefill chunks.
 //  * k_attn_combine: joins each row's pieces (the key axis is cut over the
 //    SMs, see attn.h) and rounds once.
 #include <cstring>
-#include <cuda.h>
 
-#include "attn.h"
-#include "ptx.cuh"
-#include "tcgen05.cuh"
+#include "attn_core.cuh"
 
 namespace tcl {
 
 namespace {
-
-__device__ __forceinline__ float pow2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -60,17 +53,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ bool bf16_pair_not_finite(uint32_t w)
-{
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 // ---------------------------------------------------------------- narrow
 
 constexpr int NA_WARPS = 4;
@@ -93,36 +75,6 @@ __device__ __forceinline__ uint32_t kv_chunk(int key, int c)
     return (uint32_t)((c >> 3) * NA_KEYS * 128 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
 }
 
-// The pieces of a CTA's run, in order.
-struct PieceWalk {
-    long long p, p1;
-    int s, h, tile0, ntiles;
-    AttnSeg g;
-    __device__ __forceinline__ PieceWalk(const AttnPlanDev &pl, int cta)
-    {
-        const long long run = pl.len[AL_RUN], all = pl.len[AL_TILES];
-        p = cta * run;
-        p1 = min(all, p + run);
-        s = p < p1 ? pl.cta_seg[cta] - 1 : 0;
-        g.a = 0;
-        g.ntiles = 0;
-        ntiles = 0;
-    }
-    __device__ __forceinline__ bool next(const AttnPlanDev &pl)
-    {
-        p += ntiles;
-        if (p >= p1)
-            return false;
-        while (p >= g.a + (long long)g.ntiles * pl.hkv)
-            g = pl.seg[++s];
-        const long long o = p - g.a;
-        h = (int)(o / g.ntiles);
-        tile0 = (int)(o - (long long)h * g.ntiles);
-        ntiles = (int)min((long long)(g.ntiles - tile0), p1 - p);
-        return true;
-    }
-};
-
 template <int D>
 __device__ void na_produce(const CUtensorMap &mk, const CUtensorMap &mv, const AttnPlanDev &p, int oob_row,
                            unsigned char *smem, uint64_t *full, uint64_t *empty, uint32_t *hide)
@@ -137,10 +89,9 @@ __device__ void na_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
     const CUtensorMap *map = side == 0 ? &mk : &mv;
     int it = 0;
     bool ok = true;
-    PieceWalk w(p, blockIdx.x);
-    while (ok && w.next(p)) {
-        const int32_t *pages = w.g.src < 0 ? p.p_pages + (long long)~w.g.src * p.max_ppages
-                                           : p.s_pages + (long long)w.g.src * p.max_spages;
+    PieceWalk w(p, AC_NARROW, blockIdx.x);
+    while (ok && w.next(p.hkv)) {
+        const int32_t *pages = pages_of(p, w.g.src);
         const int nkeys = w.g.nkeys;
         int key = w.tile0 * NA_KEYS + box * br;
         int page = mine && key < nkeys ? pages[key >> p.page_log2] : -1;
@@ -179,7 +130,7 @@ __device__ __forceinline__ void na_bar() { asm volatile("bar.sync 1, %0;" ::"n"(
 template <int D>
 __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
     k_attn_narrow(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const AttnPlanDev p, const AttnArgs a)
+                  const AttnPlanDev p, const AttnArgs a, const bool after_wide)
 {
     typedef NaShape<D> S;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -196,10 +147,16 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_wait();  // the plan, q and the cache; the partial rows' last reader
+    // the plan, q and the cache; the partial rows' last reader.  After the wide kernel all of it is there: each of
+    // its CTAs let this kernel start only once it had waited itself.  The two work side by side, and this one
+    // ends after it, so that the combine kernel's wait covers both.
+    if (!after_wide)
+        pdl_wait();
     pdl_launch_dependents();
     if (warp == NA_WARPS) {
         na_produce<D>(mk, mv, p, a.oob_row, smem, full, empty, hide);
+        if (after_wide)
+            pdl_wait();
         return;
     }
     int32_t *status = p.hdr + AH_STATUS;
@@ -211,8 +168,8 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
     const uint32_t ring = smem_u32(smem);
     int it = 0;
     bool ok = true;  // no wait has run out
-    PieceWalk w(p, blockIdx.x);
-    while (w.next(p)) {
+    PieceWalk w(p, AC_NARROW, blockIdx.x);
+    while (w.next(p.hkv)) {
         const AttnSeg &g = w.g;
         // the rows' queries, in the product's operand layout
         uint32_t qa[D / 16][4];
@@ -439,9 +396,8 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const
     const int t = (int)(row / p.hq), hq = (int)(row % p.hq), G = p.hq / p.hkv, h = hq / G;
     const int b = p.tok_req[t];
     long long base[2] = {0, 0};
-    int c0[2] = {0, 0}, n[2] = {0, 0};
+    int pitch[2] = {0, 0}, n[2] = {0, 0};
     if (b >= 0) {
-        const long long run = p.len[AL_RUN];
         const int grp = p.grp[b];
         const int first[2] = {grp >= 0 ? p.pseg[grp] : -1, p.sseg[b]};
         const int t0[2] = {grp >= 0 ? p.g_row0[grp] : 0, p.q_off[b]};
@@ -449,20 +405,26 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const
         for (int k = 0; k < 2; ++k) {
             if (first[k] < 0)
                 continue;
+            const int cls = first[k] & 1, tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS;
+            const long long *len = p.len + cls * AL_WORDS;
             const int r = (t - t0[k]) * G + hq % G;
-            const AttnSeg &g = p.seg[first[k] + r / NA_ROWS];
+            const AttnSeg &g = p.seg[cls][(first[k] >> 1) + r / tr];
             if (g.ntiles == 0)
                 continue;
-            const long long a0 = g.a + (long long)h * g.ntiles;
-            c0[k] = (int)(a0 / run);
-            n[k] = (int)((a0 + g.ntiles - 1) / run) - c0[k] + 1;
-            base[k] = (long long)c0[k] * NA_ROWS + g.rows0 + (long long)h * g.nrows + r % NA_ROWS;
+            const long long a0 = g.a + (long long)h * g.ntiles, run = len[AL_RUN];
+            const int c0 = (int)(a0 / run);
+            n[k] = (int)((a0 + g.ntiles - 1) / run) - c0 + 1;
+            pitch[k] = p.pitch[cls];
+            base[k] = len[AL_PART] + (long long)c0 * pitch[k] + g.rows0 + (long long)h * g.nrows + r % tr;
         }
     }
+    auto part_row = [&](int i) {
+        return i < n[0] ? base[0] + (long long)i * pitch[0] : base[1] + (long long)(i - n[0]) * pitch[1];
+    };
     const int np = n[0] + n[1];
     float M = -INFINITY;
     for (int i = lane; i < np; i += 32)
-        M = fmaxf(M, p.part_ml[i < n[0] ? base[0] + (long long)i * NA_ROWS : base[1] + (long long)(i - n[0]) * NA_ROWS].x);
+        M = fmaxf(M, p.part_ml[part_row(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -470,7 +432,7 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const
     float acc[E] = {}, L = 0.f;
 #pragma unroll 4
     for (int i = 0; i < np; ++i) {
-        const long long pr = i < n[0] ? base[0] + (long long)i * NA_ROWS : base[1] + (long long)(i - n[0]) * NA_ROWS;
+        const long long pr = part_row(i);
         const float2 ml = p.part_ml[pr];
         const float w = pow2(ml.x - B);
         L += w * ml.y;
@@ -498,22 +460,6 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const
         a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945f;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D>
 cudaError_t run_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)
 {
@@ -533,7 +479,16 @@ cudaError_t run_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cach
     CUtensorMap mk, mv;
     std::memcpy(&mk, cache.map_k, sizeof(mk));
     std::memcpy(&mv, cache.map_v, sizeof(mv));
-    cudaError_t e = launch_pdl(k_attn_narrow<D>, dim3(p.ctas), NA_THREADS, NaShape<D>::SMEM, st, mk, mv, p, a);
+    // which classes there can be: a request's rows are its tokens times the heads that share a key/value head
+    const int G = p.hq / p.hkv;
+    const bool wide = (long long)a.TQ * G > NA_ROWS;
+    const bool narrow = G <= NA_ROWS && (!wide || a.B > 1);
+    cudaError_t e = cudaSuccess;
+    if (wide)
+        e = launch_attn_wide(p, a, mk, mv, cache.v, st);
+    if (e == cudaSuccess && narrow)
+        e = launch_pdl(k_attn_narrow<D>, dim3(p.ctas[AC_NARROW]), NA_THREADS, NaShape<D>::SMEM, st, mk, mv, p, a,
+                       wide);
     if (e != cudaSuccess)
         return e;
     const long long rows = (long long)a.TQ * p.hq;
@@ -578,6 +533,7 @@ lora_status lora_prefix_attention(const void *q_dev, long long q_stride, void *o
     a.out_stride = out_stride;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.TQ = plan->TQ;
+    a.B = plan->B;
     a.oob_row = cache->num_pages * cache->hkv * cache->page_size;
     return launch_attn(p, a, *cache, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }

@@ -2,6 +2,8 @@
 // their translation units.
 #pragma once
 
+#include <cuda.h>
+
 #include "internal.h"
 
 struct lora_kv_cache {
@@ -22,20 +24,25 @@ constexpr int ATTN_BOX_MAX = 64;
 // read the same keys -- a group's prefix, or a request's own tokens --
 // the same for every key/value head.
 //
-// The narrow kernel takes tiles of NA_ROWS rows and NA_KEYS keys.  All tiles
-// of all segments and heads stand in one sequence, segment by segment, head
-// by head, in the order of the keys; each CTA takes an equal run of them, so
-// a segment of a head is cut into pieces by the runs' ends.  A piece's
-// result (the rows' unnormalised sums, running maximum and sum) goes to
-// partial rows of its own, CTA * NA_ROWS + rows0 + head * nrows on: the row
-// counter grows by at least nrows from a piece to the next one.
+// Groups and requests of at most NA_ROWS rows go to the narrow kernel (tiles
+// of 16 rows and 64 keys), the others to the wide one (256 rows, 128 keys).
+// Of each class, all tiles of all segments and heads stand in one sequence,
+// segment by segment, head by head, in the order of the keys; each CTA takes
+// an equal run of them, so a segment of a head is cut into pieces by the
+// runs' ends.  A piece's result (the rows' unnormalised sums, running
+// maximum and sum) goes to partial rows of its own, from CTA * pitch + rows0
+// + head * nrows on (pitch: the most rows of a tile): the row counter grows
+// by at least nrows from a piece to the next one.
 constexpr int NA_ROWS = 16;
 constexpr int NA_KEYS = 64;
 constexpr int NA_CTAS_PER_SM = 2;
+constexpr int WA_ROWS = 256;
+constexpr int WA_KEYS = 128;
+enum { AC_NARROW = 0, AC_WIDE = 1 };  // class of a segment
 
 struct AttnSeg {
     long long a;      // first tile of head 0 in the sequence
-    long long rows0;  // query rows of the segments before, over all heads
+    long long rows0;  // its class's query rows of the segments before, over all heads
     int row0;         // first row: token * (hq / hkv) + head of the group
     int nrows;
     int nkeys;        // keys that some row sees
@@ -45,31 +52,31 @@ struct AttnSeg {
 };
 
 // Header words of a plan (device int32).
-enum { AH_STATUS = 0, AH_NREQ = 1, AH_NGRP = 2, AH_NSEG = 3, AH_WORDS = 16 };
-// The sequence's length and each CTA's run (device int64).
-enum { AL_TILES = 0, AL_RUN = 1, AL_WORDS = 4 };
+enum { AH_STATUS = 0, AH_NREQ = 1, AH_NGRP = 2, AH_WORDS = 16 };
+// Per class: its sequence's length, each CTA's run, its first partial row (device int64).
+enum { AL_TILES = 0, AL_RUN = 1, AL_PART = 2, AL_WORDS = 4 };
 
 // A plan on the device.  Lengths are already checked against their tables:
 // a request's or group's length is 0 where it was malformed, a page is -1
 // where its id was.
 struct AttnPlanDev {
     int32_t *hdr;      // [AH_WORDS]
-    long long *len;    // [AL_WORDS]
+    long long *len;    // [2][AL_WORDS]
     int32_t *q_off;    // [max_requests + 1]
     int32_t *grp;      // [max_requests] group of each request, -1: none
     int32_t *g_row0;   // [max_groups] first query token of the group
     int32_t *tok_req;  // [max_queries] request of each query token, -1: none
-    int32_t *sseg;     // [max_requests] first segment of the request's own tokens, -1: none
-    int32_t *pseg;     // [max_groups] first segment of the group's prefix, -1: none
+    int32_t *sseg;     // [max_requests] 2 * first segment of the request's own tokens + class, -1: none
+    int32_t *pseg;     // [max_groups] the same of the group's prefix
     int32_t *s_pages;  // [max_requests][max_spages]
     int32_t *p_pages;  // [max_groups][max_ppages]
-    AttnSeg *seg;      // [max_segs]
-    int32_t *cta_seg;  // [ctas] segment in which each CTA's run begins
+    AttnSeg *seg[2];      // [max_segs] per class
+    int32_t *cta_seg[2];  // [ctas] segment in which each CTA's run begins
     float *part;       // [part_rows][d]
     float2 *part_ml;   // [part_rows] running maximum (in units of log 2) and sum
     int max_spages, max_ppages, max_segs;
     int hq, hkv, d, page, page_log2;
-    int ctas;
+    int ctas[2], pitch[2];
 };
 
 struct AttnPlanSrc {
@@ -85,16 +92,18 @@ struct AttnArgs {
     float *lse;
     long long q_stride, out_stride;
     float scale_log2;  // scale / log 2: weights are powers of two
-    int TQ;
+    int TQ, B;
     int oob_row;       // a row outside the cache: its loads give zeros
 };
 cudaError_t launch_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                             const __nv_bfloat16 *vcache, cudaStream_t st);
 
 }  // namespace tcl
 
 struct lora_attn_plan {
     int max_requests, max_groups, max_queries, device;
-    int TQ, num_pages;
+    int TQ, B, num_pages;
     bool built;
     tcl::AttnPlanDev dev;
 };

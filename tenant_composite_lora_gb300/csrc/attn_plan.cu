@@ -73,10 +73,10 @@ struct Reader {
     int t0, n, len, lim;
 };
 
-// Keys that the last row of row tile k sees.
-__device__ __forceinline__ int tile_keys(const Reader &r, int G, int k)
+// Keys that the last row of row tile k (of `rows` rows) sees.
+__device__ __forceinline__ int tile_keys(const Reader &r, int G, int rows, int k)
 {
-    const int last = min(r.n * G, (k + 1) * NA_ROWS) - 1;
+    const int last = min(r.n * G, (k + 1) * rows) - 1;
     return max(0, min(r.len, r.t0 + last / G + r.lim));
 }
 
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
         }
         // the segments: groups, then requests
         const int G = p.hq / p.hkv;
-        long long segs = 0, tiles = 0, rows = 0;
+        long long segs[2] = {0, 0}, tiles[2] = {0, 0}, rows[2] = {0, 0};
         for (int i0 = 0; i0 < NG + B; i0 += AP_THREADS) {
             const int i = i0 + tid;
             Reader r{0, 0, 0, 0};
@@ -132,54 +132,71 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                 r.len = checked_len(s.s_len[b], s.s_stride, p.page, status);
                 r.lim = r.len - r.n + 1 - r.t0;
             }
-            const int nt = r.len > 0 ? (int)(((long long)r.n * G + NA_ROWS - 1) / NA_ROWS) : 0;
+            const int all_rows = r.len > 0 ? r.n * G : 0;
+            const int cls = all_rows > NA_ROWS ? AC_WIDE : AC_NARROW;
+            const int tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS, tk = cls == AC_WIDE ? WA_KEYS : NA_KEYS;
+            const int nt = (all_rows + tr - 1) / tr;
             long long my_tiles = 0;
             for (int k = 0; k < nt; ++k)
-                my_tiles += (tile_keys(r, G, k) + NA_KEYS - 1) / NA_KEYS;
-            long long all;
-            long long seg0 = segs + block_before(nt, all, sh);
-            segs += all;
-            long long a = tiles + p.hkv * block_before(my_tiles, all, sh);
-            tiles += p.hkv * all;
-            long long row = rows + p.hkv * block_before(nt > 0 ? (long long)r.n * G : 0, all, sh);
-            rows += p.hkv * all;
+                my_tiles += (tile_keys(r, G, tr, k) + tk - 1) / tk;
+            long long seg0 = 0, a = 0, row = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                long long all;
+                const bool is = cls == c;
+                const long long s0 = segs[c] + block_before(is ? nt : 0, all, sh);
+                segs[c] += all;
+                const long long a0 = tiles[c] + p.hkv * block_before(is ? my_tiles : 0, all, sh);
+                tiles[c] += p.hkv * all;
+                const long long row0 = rows[c] + p.hkv * block_before(is ? all_rows : 0, all, sh);
+                rows[c] += p.hkv * all;
+                if (is) {
+                    seg0 = s0;
+                    a = a0;
+                    row = row0;
+                }
+            }
             if (i < NG)
-                p.pseg[i] = nt > 0 ? (int)seg0 : -1;
+                p.pseg[i] = nt > 0 ? 2 * (int)seg0 + cls : -1;
             else if (i < NG + B)
-                p.sseg[i - NG] = nt > 0 ? (int)seg0 : -1;
+                p.sseg[i - NG] = nt > 0 ? 2 * (int)seg0 + cls : -1;
             for (int k = 0; k < nt; ++k) {
                 AttnSeg g;
                 g.a = a;
                 g.rows0 = row;
-                g.row0 = r.t0 * G + k * NA_ROWS;
-                g.nrows = min(NA_ROWS, r.n * G - k * NA_ROWS);
-                g.nkeys = tile_keys(r, G, k);
-                g.ntiles = (g.nkeys + NA_KEYS - 1) / NA_KEYS;
+                g.row0 = r.t0 * G + k * tr;
+                g.nrows = min(tr, all_rows - k * tr);
+                g.nkeys = tile_keys(r, G, tr, k);
+                g.ntiles = (g.nkeys + tk - 1) / tk;
                 g.src = i < NG ? ~i : i - NG;
                 g.lim = r.lim;
-                p.seg[seg0 + k] = g;
+                p.seg[cls][seg0 + k] = g;
                 a += (long long)p.hkv * g.ntiles;
                 row += (long long)p.hkv * g.nrows;
             }
         }
-        const long long run = (tiles + p.ctas - 1) / p.ctas;
-        if (tid == 0) {
-            p.hdr[AH_NSEG] = (int)segs;
-            p.len[AL_TILES] = tiles;
-            p.len[AL_RUN] = run;
-        }
         __syncthreads();  // the segments are written (by this block)
-        for (int c = tid; c < p.ctas; c += AP_THREADS) {
-            const long long at = c * run;
-            int lo = 0, hi = (int)segs;  // last segment starting at or before `at`: the one that holds it
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.seg[mid].a <= at)
-                    lo = mid;
-                else
-                    hi = mid;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const long long run = (tiles[c] + p.ctas[c] - 1) / p.ctas[c];
+            if (tid == 0) {
+                p.len[c * AL_WORDS + AL_TILES] = tiles[c];
+                p.len[c * AL_WORDS + AL_RUN] = run;
+                p.len[c * AL_WORDS + AL_PART] =
+                    c == AC_NARROW ? 0 : (long long)p.ctas[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
             }
-            p.cta_seg[c] = lo;
+            for (int x = tid; x < p.ctas[c]; x += AP_THREADS) {
+                const long long at = x * run;
+                int lo = 0, hi = (int)segs[c];  // last segment starting at or before `at`: the one that holds it
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (p.seg[c][mid].a <= at)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                p.cta_seg[c][x] = lo;
+            }
         }
         return;
     }
@@ -233,8 +250,8 @@ void free_plan(lora_attn_plan *p)
     if (!p)
         return;
     AttnPlanDev &d = p->dev;
-    void *all[] = {d.hdr,  d.len,     d.q_off,   d.grp, d.g_row0,  d.tok_req, d.sseg,
-                   d.pseg, d.s_pages, d.p_pages, d.seg, d.cta_seg, d.part,    d.part_ml};
+    void *all[] = {d.hdr,     d.len,    d.q_off,  d.grp,        d.g_row0,     d.tok_req, d.sseg,   d.pseg,
+                   d.s_pages, d.p_pages, d.seg[0], d.seg[1], d.cta_seg[0], d.cta_seg[1], d.part,    d.part_ml};
     for (void *x : all)
         if (x)
             cudaFree(x);
@@ -284,13 +301,17 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     d.d = head_dim;
     d.page = page_size;
     d.page_log2 = __builtin_ctz((unsigned)page_size);
-    d.ctas = NA_CTAS_PER_SM * sm_count();
+    d.ctas[AC_NARROW] = NA_CTAS_PER_SM * sm_count();
+    d.ctas[AC_WIDE] = sm_count();
     // a row tile of every group and request and one per full tile of rows;
     // a query row has partial rows for the prefix and the request's own
     // tokens, and each end of a CTA's run splits one row tile
     const long long tokens_rows = (long long)max_queries * (n_q_heads / n_kv_heads);
-    const long long segs = (long long)max_groups + max_requests + 2 * (tokens_rows / NA_ROWS + 1);
-    const long long part_rows = (long long)d.ctas * NA_ROWS + 2ll * max_queries * n_q_heads;
+    const long long segs = (long long)max_groups + max_requests + 2 * (tokens_rows / WA_ROWS + 1);
+    d.pitch[AC_NARROW] = NA_ROWS;
+    d.pitch[AC_WIDE] = (int)(tokens_rows < WA_ROWS ? tokens_rows : WA_ROWS);
+    const long long part_rows = (long long)d.ctas[AC_NARROW] * d.pitch[AC_NARROW] +
+                                (long long)d.ctas[AC_WIDE] * d.pitch[AC_WIDE] + 2ll * max_queries * n_q_heads;
     if (segs > 0x7fffffffll || tokens_rows > 0x3fffffffll) {
         free_plan(p);
         return LORA_ERR_NOT_SUPPORTED;
@@ -306,8 +327,10 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     if (e == cudaSuccess) e = plan_alloc(&d.tok_req, (size_t)max_queries);
     if (e == cudaSuccess) e = plan_alloc(&d.s_pages, (size_t)max_requests * max_suffix_pages);
     if (e == cudaSuccess) e = plan_alloc(&d.p_pages, (size_t)max_groups * max_prefix_pages);
-    if (e == cudaSuccess) e = plan_alloc(&d.seg, (size_t)segs);
-    if (e == cudaSuccess) e = plan_alloc(&d.cta_seg, (size_t)d.ctas);
+    for (int c = 0; c < 2; ++c) {
+        if (e == cudaSuccess) e = plan_alloc(&d.seg[c], (size_t)segs);
+        if (e == cudaSuccess) e = plan_alloc(&d.cta_seg[c], (size_t)d.ctas[c]);
+    }
     if (e == cudaSuccess) e = plan_alloc(&d.part, (size_t)part_rows * head_dim);
     if (e == cudaSuccess) e = plan_alloc(&d.part_ml, (size_t)part_rows);
     if (e == cudaSuccess) e = cudaMemset(d.hdr, 0, AH_WORDS * sizeof(int32_t));
@@ -339,6 +362,7 @@ lora_status lora_attn_plan_build(lora_attn_plan *plan, const int32_t *q_offsets_
     if (e != cudaSuccess)
         return status_of(e);
     plan->TQ = TQ;
+    plan->B = B;
     plan->num_pages = num_pages;
     plan->built = true;
     return LORA_OK;

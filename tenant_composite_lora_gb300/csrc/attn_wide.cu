@@ -1,0 +1,482 @@
+// The attention's wide kernel: segments of more than 16 query rows -- a
+// prefix behind many requests, a prefill chunk, a request with many heads per
+// key/value head -- on tcgen05.
+//
+// A CTA per SM walks its run of (256 rows x 128 keys) tiles:
+//  * warp 8 brings the tiles' keys and values, page by page, by TMA through a
+//    ring of 32 KB slots (keys, values, keys, ... in turn);
+//  * warp 9 (one thread) issues the products: S = Q K^T of both 128-row
+//    halves into tensor memory, later O += P V with P read from tensor
+//    memory, where it replaces S;
+//  * warps 0-3 and 4-7 own a half each, a thread per row: S is read into
+//    registers, the weights 2^(s - m) go back as P in bf16 while the other
+//    half's products run, so the tensor cores and the exponentials overlap.
+// The reference m follows the running maximum only when that has grown by
+// more than 2^8 (a weight is then at most 2^8, harmless in fp32 sums and in
+// bf16, which has the same range): O is rescaled in tensor memory only then.
+// P in bf16 is the one rounding: the product takes both operands in one
+// type, and v is bf16.
+//
+// Bound, from 128 rows up, by the products (4 of 128 x 128 x D a tile) and
+// the exponentials (256 x 128 a tile) about alike; below by the cache's bytes.
+#include "attn_core.cuh"
+
+namespace tcl {
+
+namespace {
+
+constexpr int WA_SOFT = 256;                // warps 0-7: a row each
+constexpr int WA_THREADS = WA_SOFT + 128;   // warp 8: TMA; warp 9: MMA; a whole warpgroup, for the register split
+constexpr int WA_HALF = 128;                // rows of one product
+constexpr float WA_SLACK = 8.f;
+// Registers: 384 threads are launched with 168 each (64,512 in all); the rows' warps take 216, the others 72.
+constexpr int WA_REGS_ROWS = 216, WA_REGS_REST = 72;
+static_assert(WA_REGS_ROWS * WA_SOFT + WA_REGS_REST * (WA_THREADS - WA_SOFT) <= 168 * WA_THREADS,
+              "the split is within what the launch holds");
+
+template <int D>
+struct WaShape {
+    static constexpr int Q = WA_ROWS * D * 2;      // both halves' queries
+    static constexpr int SLOT = WA_KEYS * D * 2;   // a tile's keys or values
+    static constexpr int SLOTS = 5 * 128 / D > 8 ? 8 : 5 * 128 / D;
+    static constexpr int SMEM = Q + SLOTS * SLOT + 1024;
+    // tensor memory columns: S of half q at 128 q (P, two bf16 a column, in its first 64), O at 256 + D q
+    static constexpr uint32_t S0 = 0, O0 = 256;
+};
+static_assert(WaShape<128>::SMEM + 256 <= 232448 && WaShape<64>::SMEM + 256 <= 232448, "shared memory of an SM");
+
+struct WaBars {
+    uint64_t full[8], empty[8];      // ring slots
+    uint64_t q_full[2];              // a half's queries are in shared memory
+    uint64_t s_full[2], p_full[2];   // its S is computed; its P is written
+    uint64_t pv_done[2];             // its O holds this tile
+    uint64_t drain;                  // all products issued have ended
+    uint32_t taddr;
+    int poison;                      // a partly seen tile of this piece holds values that are not finite
+};
+
+__device__ __forceinline__ void wa_bar_half(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half)); }
+__device__ __forceinline__ void wa_bar_both() { asm volatile("bar.sync 3, %0;" ::"n"(WA_SOFT) : "memory"); }
+
+// ---- producer warp
+template <int D>
+__device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const AttnPlanDev &p, int oob_row,
+                           unsigned char *ring, WaBars &bar)
+{
+    typedef WaShape<D> S;
+    const int lane = threadIdx.x & 31;
+    int32_t *status = p.hdr + AH_STATUS;
+    const int br = min(p.page, ATTN_BOX_MAX), nb = WA_KEYS / br;
+    const int per = nb * (D / 64);  // boxes of a slot: at most 16
+    const int box = lane % nb, col = (lane / nb) % (D / 64);
+    const bool mine = lane < per;
+    int it = 0;  // slots filled
+    bool ok = true;
+    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    while (ok && w.next(p.hkv)) {
+        const int32_t *pages = pages_of(p, w.g.src);
+        const int nkeys = w.g.nkeys;
+        int key = w.tile0 * WA_KEYS + box * br;
+        int page = mine && key < nkeys ? pages[key >> p.page_log2] : -1;
+        for (int k = 0; ok && k < w.ntiles; ++k) {
+            const int nkey = key + WA_KEYS;
+            const int npage = mine && k + 1 < w.ntiles && nkey < nkeys ? pages[nkey >> p.page_log2] : -1;
+            const bool live = mine && key < nkeys;
+            const unsigned lives = __ballot_sync(0xffffffffu, live);
+            const int row = page < 0 ? oob_row : (page * p.hkv + w.h) * p.page + (key & (p.page - 1));
+            for (int side = 0; side < 2; ++side, ++it) {
+                const int s = it % S::SLOTS;
+                if (it >= S::SLOTS && !mbar_wait_bounded(&bar.empty[s], ((it / S::SLOTS) - 1) & 1, status)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&bar.full[s], (uint32_t)__popc(lives) * br * 128);
+                __syncwarp();
+                if (live)
+                    tma_load_2d(ring + s * S::SLOT + col * WA_KEYS * 128 + box * br * 128, side ? &mv : &mk, col * 64,
+                                row, &bar.full[s]);
+            }
+            key = nkey;
+            page = npage;
+        }
+    }
+    // every load has landed before the CTA can exit
+    for (int i = max(0, it - S::SLOTS); i < it && ok; ++i)
+        ok = mbar_wait_bounded(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status);
+}
+
+// ---- MMA thread
+template <int D>
+__device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars &bar)
+{
+    typedef WaShape<D> S;
+    int32_t *status = p.hdr + AH_STATUS;
+    const uint32_t t = bar.taddr;
+    const uint32_t id_qk = umma_idesc_bf16(WA_HALF, WA_KEYS);
+    const uint32_t id_pv = umma_idesc_bf16(WA_HALF, D) | (1u << 16);  // B = V: MN-major
+    int it = 0;  // slots consumed
+    int nq[2] = {0, 0}, np[2] = {0, 0};
+    auto scores = [&](int q, uint32_t k) {  // S_q = Q_q K^T
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * (WA_HALF * 128) + (kk & 3) * 32;
+            umma_bf16(t + S::S0 + q * 128, umma_desc_sw128(qs + q * (WA_HALF * D * 2) + off),
+                      umma_desc_sw128(k + off), id_qk, kk > 0);
+        }
+        umma_commit(&bar.s_full[q]);
+    };
+    auto slot_full = [&](int i) { return mbar_wait_bounded(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status); };
+    bool ok = true;
+    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    while (ok && w.next(p.hkv)) {
+        const int halves = w.g.nrows > WA_HALF ? 2 : 1;
+        ok = slot_full(it);
+        for (int q = 0; ok && q < halves; ++q) {
+            ok = mbar_wait_bounded(&bar.q_full[q], nq[q]++ & 1, status);
+            tc_fence_after();
+            if (ok)
+                scores(q, ring + (it % S::SLOTS) * S::SLOT);
+        }
+        if (!ok)
+            break;
+        umma_commit(&bar.empty[it % S::SLOTS]);
+        ++it;
+        for (int k = 0; ok && k < w.ntiles; ++k) {
+            // now: it = this tile's values, it + 1 = the next tile's keys
+            const bool more = k + 1 < w.ntiles;
+            const uint32_t v = ring + (it % S::SLOTS) * S::SLOT, kn = ring + ((it + 1) % S::SLOTS) * S::SLOT;
+            ok = slot_full(it) && (!more || slot_full(it + 1));
+            for (int q = 0; ok && q < halves; ++q) {
+                ok = mbar_wait_bounded(&bar.p_full[q], np[q] & 1, status);
+                if (!ok)
+                    break;
+                ++np[q];
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < WA_KEYS / 16; ++kk)
+                    umma_bf16_ta(t + S::O0 + q * D, t + S::S0 + q * 128 + kk * 8,
+                                 umma_desc_sw128_mn(v + kk * 2048, WA_KEYS * 128, 1024), id_pv, k > 0 || kk > 0);
+                umma_commit(&bar.pv_done[q]);
+                if (more)
+                    scores(q, kn);
+            }
+            if (!ok)
+                break;
+            umma_commit(&bar.empty[it % S::SLOTS]);
+            ++it;
+            if (more) {
+                umma_commit(&bar.empty[it % S::SLOTS]);
+                ++it;
+            }
+        }
+    }
+    umma_commit(&bar.drain);
+    mbar_wait_bounded(&bar.drain, 0, status);
+}
+
+// ---- softmax warps: thread = row
+template <int D>
+__device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_bfloat16 *vcache, unsigned char *qsm,
+                           unsigned char *ring, WaBars &bar)
+{
+    typedef WaShape<D> S;
+    const int tid = threadIdx.x, half = tid >> 7, r = tid & 127, lane = tid & 31;
+    int32_t *status = p.hdr + AH_STATUS;
+    const int G = p.hq / p.hkv;
+    const bool bad_pages = (*(volatile int32_t *)status & LORA_DEV_BAD_PAGE) != 0;
+    const uint32_t quarter = (uint32_t)((r >> 5) * 32) << 16;  // this warp's tensor memory lanes
+    const uint32_t ts = bar.taddr + quarter + S::S0 + half * 128, to = bar.taddr + quarter + S::O0 + half * D;
+    // 2^(s * c - m) wants c > 0: a negative scale turns the queries' signs, a scale of 0 makes them 0
+    const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+    const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u, q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    int nt = 0;    // tiles of this half so far
+    int it = 0;    // ring slots so far
+    // once a wait has run out (ok is the same in all lanes of a warp) only the barriers are still met
+    bool ok = true;
+    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    while (w.next(p.hkv)) {
+        const AttnSeg &g = w.g;
+        const bool active = half * WA_HALF < g.nrows;
+        if (active) {
+            // this half's queries; the products that read the ones before have ended (their S was waited for)
+            for (int i = r; i < WA_HALF * (D / 8); i += 128) {
+                const int row = i / (D / 8), ch = i % (D / 8), rr = half * WA_HALF + row;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (rr < g.nrows) {
+                    const int gr = g.row0 + rr, t = gr / G;
+                    x = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (long long)(w.h * G + gr % G) * D +
+                                                         ch * 8);
+                    x.x = (x.x & q_and) ^ q_xor;
+                    x.y = (x.y & q_and) ^ q_xor;
+                    x.z = (x.z & q_and) ^ q_xor;
+                    x.w = (x.w & q_and) ^ q_xor;
+                }
+                *reinterpret_cast<uint4 *>(qsm + half * (WA_HALF * D * 2) + sw128_offset(row, ch * 8, WA_HALF)) = x;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar.q_full[half]);
+        } else {
+            it += 2 * w.ntiles;
+            continue;
+        }
+        const int row = half * WA_HALF + r;
+        const bool valid = row < g.nrows;
+        const int lim = valid ? min(g.nkeys, max(0, (g.row0 + row) / G + g.lim)) : g.nkeys;
+        const int lim_first = min(g.nkeys, max(0, g.row0 / G + g.lim));  // of the segment's first row: the least
+        const int piece_end = min(g.nkeys, (w.tile0 + w.ntiles) * WA_KEYS);
+        const bool partly = piece_end > lim_first;  // some row does not see all of the piece
+        if (partly && half == 0) {
+            if (tid == 0)
+                bar.poison = 0;
+            wa_bar_half(0);
+        }
+        float m = -INFINITY, l = 0.f;
+        for (int k = 0; ok && k < w.ntiles; ++k, ++nt, it += 2) {
+            ok = mbar_wait_bounded(&bar.s_full[half], nt & 1, status);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_ld32_nowait(ts + i * 32, s[i]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_landed(s[i]);
+            const int key0 = (w.tile0 + k) * WA_KEYS;
+            if (__any_sync(0xffffffffu, key0 + WA_KEYS > lim)) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (key0 + i >= lim)
+                        s[i >> 5][i & 31] = 0xff800000u;  // -inf
+            }
+            if (bad_pages) {
+                const int32_t *pages = pages_of(p, g.src);
+#pragma unroll
+                for (int i = 0; i < 128; i += 16)
+                    if (key0 + i < g.nkeys && pages[(key0 + i) >> p.page_log2] < 0)
+#pragma unroll
+                        for (int j = i; j < i + 16; ++j)
+                            s[j >> 5][j & 31] = 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
+            const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+            if (k == 0) {
+                m = mnew;
+            } else if (__any_sync(0xffffffffu, mnew > m + WA_SLACK)) {
+                // O and the sum move to the new reference
+                const float f = m == mnew ? 1.f : pow2(m - mnew);
+                m = mnew;
+                l *= f;
+                ok = mbar_wait_bounded(&bar.pv_done[half], (nt - 1) & 1, status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(to + i, o);
+                    tmem_wait_ld();
+                    tmem_landed(o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st32(to + i, o);
+                }
+            }
+            const float nb = m == -INFINITY ? 0.f : -m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float x = pow2(fmaf(__uint_as_float(s[2 * i + (j >> 4)][(2 * j) & 31]), c, nb));
+                    const float y = pow2(fmaf(__uint_as_float(s[2 * i + (j >> 4)][(2 * j + 1) & 31]), c, nb));
+                    sum[(2 * j) & 3] += x;
+                    sum[(2 * j + 1) & 3] += y;
+                    pk[j] = pack_bf16(x, y);
+                }
+                tmem_st32(ts + i * 32, pk);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            // the first half sees to the values: beyond the keys they count as 0, whatever they hold; one that is
+            // not finite and that only some rows see is taken out here and added to those rows at the end
+            if (half == 0 && key0 + WA_KEYS > lim_first) {
+                const int vs = it + 1;
+                ok = mbar_wait_bounded(&bar.full[vs % S::SLOTS], (vs / S::SLOTS) & 1, status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char *v = ring + (vs % S::SLOTS) * S::SLOT;
+                bool odd = false;
+                for (int i = r; i < WA_KEYS * (D / 8); i += 128) {
+                    const int key = i / (D / 8), ch = i % (D / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(v + (ch >> 3) * WA_KEYS * 128 + key * 128 +
+                                                          (((ch & 7) ^ (key & 7)) << 4));
+                    if (key0 + key >= g.nkeys) {
+                        *at = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 x = *at;
+                    if (bf16_pair_not_finite(x.x) || bf16_pair_not_finite(x.y) || bf16_pair_not_finite(x.z) ||
+                        bf16_pair_not_finite(x.w)) {
+                        uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (bf16_not_finite(e[j]))
+                                e[j] &= 0xffff0000u;
+                            if (bf16_not_finite(e[j] >> 16))
+                                e[j] &= 0x0000ffffu;
+                        }
+                        *at = make_uint4(e[0], e[1], e[2], e[3]);
+                        odd = true;
+                    }
+                }
+                if (odd)
+                    bar.poison = 1;
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar.p_full[half]);
+        }
+        // the piece's result
+        ok = ok && mbar_wait_bounded(&bar.pv_done[half], (nt - 1) & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        bool poison = false;
+        if (partly) {
+            const bool both = g.nrows > WA_HALF;
+            both ? wa_bar_both() : wa_bar_half(0);
+            poison = *(volatile int *)&bar.poison != 0;
+            both ? wa_bar_both() : wa_bar_half(0);  // read by all before the next piece clears it
+        }
+        if (!ok)
+            continue;
+        const long long out =
+            p.len[AC_WIDE * AL_WORDS + AL_PART] + (long long)blockIdx.x * p.pitch[AC_WIDE] + g.rows0 +
+            (long long)w.h * g.nrows + row;
+        if (valid)
+            p.part_ml[out] = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32_nowait(to + i, o);
+            tmem_wait_ld();
+            tmem_landed(o);
+            if (poison && valid) {
+                const int32_t *pages = pages_of(p, g.src);
+                for (int key = max(w.tile0 * WA_KEYS, lim_first / WA_KEYS * WA_KEYS); key < min(lim, piece_end); ++key) {
+                    const int pg = pages[key >> p.page_log2];
+                    if (pg < 0)
+                        continue;
+                    const uint32_t *x = reinterpret_cast<const uint32_t *>(
+                        vcache + (((long long)pg * p.hkv + w.h) * p.page + (key & (p.page - 1))) * D + i);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t e = x[j];
+                        if (bf16_not_finite(e))
+                            o[2 * j] = __float_as_uint(__uint_as_float(o[2 * j]) + bf16lo(e));
+                        if (bf16_not_finite(e >> 16))
+                            o[2 * j + 1] = __float_as_uint(__uint_as_float(o[2 * j + 1]) + bf16hi(e));
+                    }
+                }
+            }
+            if (valid) {
+                uint4 *x = reinterpret_cast<uint4 *>(p.part + out * D + i);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+        }
+        tc_fence_before();
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(WA_THREADS, 1)
+    k_attn_wide(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnPlanDev p,
+                const AttnArgs a, const __nv_bfloat16 *vcache)
+{
+    typedef WaShape<D> S;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~static_cast<uintptr_t>(1023));
+    __shared__ WaBars bar;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < S::SLOTS; ++s) {
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], 1);
+        }
+        for (int q = 0; q < 2; ++q) {
+            mbar_init(&bar.q_full[q], 128);
+            mbar_init(&bar.s_full[q], 1);
+            mbar_init(&bar.p_full[q], 128);
+            mbar_init(&bar.pv_done[q], 1);
+        }
+        mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9)
+        tmem_alloc(&bar.taddr, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();  // the plan, q and the cache; the partial rows' last reader
+    pdl_launch_dependents();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WA_REGS_ROWS));
+        wa_softmax<D>(p, a, vcache, smem, smem + S::Q, bar);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WA_REGS_REST));
+        if (warp == 8)
+            wa_produce<D>(mk, mv, p, a.oob_row, smem + S::Q, bar);
+        else if (warp == 9 && lane == 0)
+            wa_mma<D>(p, smem_u32(smem), smem_u32(smem + S::Q), bar);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9)
+        tmem_dealloc(bar.taddr, 512);
+}
+
+template <int D>
+cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                     const __nv_bfloat16 *vcache, cudaStream_t st)
+{
+    static thread_local int attr_dev = -1;  // per host thread
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (attr_dev != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(k_attn_wide<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   WaShape<D>::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        attr_dev = dev;
+    }
+    return launch_pdl(k_attn_wide<D>, dim3(p.ctas[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, p, a, vcache);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                             const __nv_bfloat16 *vcache, cudaStream_t st)
+{
+    return p.d == 64 ? run_wide<64>(p, a, mk, mv, vcache, st) : run_wide<128>(p, a, mk, mv, vcache, st);
+}
+
+}  // namespace tcl
