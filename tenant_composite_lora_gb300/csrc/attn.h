@@ -2,21 +2,20 @@
 // their translation units.
 #pragma once
 
-#include <cuda.h>
-
 #include "internal.h"
 
 struct lora_kv_cache {
     int num_pages, page_size, hkv, d;
     __nv_bfloat16 *k, *v;  // [num_pages][hkv][page_size][d], the caller's
-    // CUtensorMap over k's and v's rows; not ready where there is no driver to encode them
-    alignas(64) unsigned char map_k[128], map_v[128];
+    // CUtensorMap over k's and v's rows, for the narrow and the wide kernel's
+    // boxes; not ready where there is no driver to encode them
+    alignas(64) unsigned char map_k[2][128], map_v[2][128];
     bool maps_ready;
 };
 
 namespace tcl {
 
-// Rows of one TMA box: a page's rows, at most 64.
+// Rows of one TMA box: the wide kernel's a page's rows, at most 64; the narrow kernel's 16.
 constexpr int ATTN_BOX_MAX = 64;
 
 // A segment of a planned batch: up to a row tile's query rows (a row is a
@@ -25,23 +24,30 @@ constexpr int ATTN_BOX_MAX = 64;
 // the same for every key/value head.
 //
 // Groups and requests of at most NA_ROWS rows go to the narrow kernel (tiles
-// of 16 rows and 64 keys), the others to the wide one (256 rows, 128 keys).
-// Of each class, all tiles of all segments and heads stand in one sequence,
-// segment by segment, head by head, in the order of the keys; each CTA takes
-// an equal run of them, so a segment of a head is cut into pieces by the
-// runs' ends.  A piece's result (the rows' unnormalised sums, running
-// maximum and sum) goes to partial rows of its own, from CTA * pitch + rows0
-// + head * nrows on (pitch: the most rows of a tile): the row counter grows
-// by at least nrows from a piece to the next one.
+// of 16 rows and 16 keys, a run of tiles per warp), the others to the wide
+// one (256 rows, 128 keys, a run per CTA).  Of each class, all tiles of all
+// segments and heads stand in one sequence, segment by segment, head by head,
+// in the order of the keys, each head's tiles after a lead of units that
+// stands for what beginning and ending a piece costs; each worker takes an
+// equal run of units, so a segment of a head is cut into pieces by the runs'
+// ends.  A piece's result (the rows' unnormalised sums, running maximum and
+// sum) goes to partial rows of its own, from worker * pitch + rows0 + head *
+// nrows on (pitch: the most rows of a tile): the row counter grows by at
+// least nrows from a piece to the next one.
 constexpr int NA_ROWS = 16;
-constexpr int NA_KEYS = 64;
-constexpr int NA_CTAS_PER_SM = 2;
+constexpr int NA_KEYS = 16;
+constexpr int NA_WARPS = 4;        // of a CTA
+constexpr int NA_CTAS_PER_SM = 3;
+constexpr int NA_LEAD = 3;         // units
+constexpr int NA_MIN_RUN = 4;
 constexpr int WA_ROWS = 256;
 constexpr int WA_KEYS = 128;
+constexpr int WA_LEAD = 2;
+constexpr int WA_MIN_RUN = 3;
 enum { AC_NARROW = 0, AC_WIDE = 1 };  // class of a segment
 
 struct AttnSeg {
-    long long a;      // first tile of head 0 in the sequence
+    long long a;      // first unit of head 0 in the sequence
     long long rows0;  // its class's query rows of the segments before, over all heads
     int row0;         // first row: token * (hq / hkv) + head of the group
     int nrows;
@@ -53,8 +59,10 @@ struct AttnSeg {
 
 // Header words of a plan (device int32).
 enum { AH_STATUS = 0, AH_NREQ = 1, AH_NGRP = 2, AH_WORDS = 16 };
-// Per class: its sequence's length, each CTA's run, its first partial row (device int64).
-enum { AL_TILES = 0, AL_RUN = 1, AL_PART = 2, AL_WORDS = 4 };
+// Per class: its sequence's units, each worker's run, its first partial row (device int64).
+enum { AL_UNITS = 0, AL_RUN = 1, AL_PART = 2, AL_WORDS = 4 };
+
+__host__ __device__ constexpr int attn_lead(int cls) { return cls == AC_WIDE ? WA_LEAD : NA_LEAD; }
 
 // A plan on the device.  Lengths are already checked against their tables:
 // a request's or group's length is 0 where it was malformed, a page is -1
@@ -62,21 +70,18 @@ enum { AL_TILES = 0, AL_RUN = 1, AL_PART = 2, AL_WORDS = 4 };
 struct AttnPlanDev {
     int32_t *hdr;      // [AH_WORDS]
     long long *len;    // [2][AL_WORDS]
-    int32_t *q_off;    // [max_requests + 1]
-    int32_t *grp;      // [max_requests] group of each request, -1: none
-    int32_t *g_row0;   // [max_groups] first query token of the group
-    int32_t *tok_req;  // [max_queries] request of each query token, -1: none
     int32_t *sseg;     // [max_requests] 2 * first segment of the request's own tokens + class, -1: none
     int32_t *pseg;     // [max_groups] the same of the group's prefix
+    int4 *tok;         // [max_queries] {pseg, the token's first row there, sseg, its first row there}
     int32_t *s_pages;  // [max_requests][max_spages]
     int32_t *p_pages;  // [max_groups][max_ppages]
     AttnSeg *seg[2];      // [max_segs] per class
-    int32_t *cta_seg[2];  // [ctas] segment in which each CTA's run begins
+    int32_t *run_seg[2];  // [workers] segment in which each worker's run begins
     float *part;       // [part_rows][d]
     float2 *part_ml;   // [part_rows] running maximum (in units of log 2) and sum
     int max_spages, max_ppages, max_segs;
     int hq, hkv, d, page, page_log2;
-    int ctas[2], pitch[2];
+    int workers[2], pitch[2];
 };
 
 struct AttnPlanSrc {
@@ -96,8 +101,7 @@ struct AttnArgs {
     int oob_row;       // a row outside the cache: its loads give zeros
 };
 cudaError_t launch_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
-cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                             const __nv_bfloat16 *vcache, cudaStream_t st);
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
 
 }  // namespace tcl
 

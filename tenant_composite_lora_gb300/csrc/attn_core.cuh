@@ -28,33 +28,72 @@ __device__ __forceinline__ bool bf16_pair_not_finite(uint32_t w)
     return bf16_not_finite(w) || bf16_not_finite(w >> 16);
 }
 
-// The pieces of a CTA's run over one class's sequence, in order.
+// mbar_wait_bounded for waits on the critical path: the test is issued again
+// at once, without a sleep between.
+__device__ __forceinline__ bool mbar_wait_now(uint64_t *bar, uint32_t parity, int32_t *status)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+            atomicOr(status, LORA_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// o / n and the remainder, for o up to 2^62 (nearly always below 2^32).
+__device__ __forceinline__ int div_units(long long o, int n, int &rem)
+{
+    if ((unsigned long long)o >> 32) {
+        const long long q = o / n;
+        rem = (int)(o - q * n);
+        return (int)q;
+    }
+    const unsigned q = (unsigned)o / (unsigned)n;
+    rem = (int)((unsigned)o - q * (unsigned)n);
+    return (int)q;
+}
+
+// The pieces of a worker's run over one class's sequence, in order.
+template <int CLS>
 struct PieceWalk {
     const AttnSeg *seg;
     long long p, p1;
     int s, h, tile0, ntiles;
     AttnSeg g;
-    __device__ __forceinline__ PieceWalk(const AttnPlanDev &pl, int cls, int cta)
+    __device__ __forceinline__ PieceWalk(const AttnPlanDev &pl, int worker)
     {
-        const long long run = pl.len[cls * AL_WORDS + AL_RUN], all = pl.len[cls * AL_WORDS + AL_TILES];
-        seg = pl.seg[cls];
-        p = cta * run;
+        const long long run = pl.len[CLS * AL_WORDS + AL_RUN], all = pl.len[CLS * AL_WORDS + AL_UNITS];
+        seg = pl.seg[CLS];
+        p = worker * run;
         p1 = min(all, p + run);
-        s = p < p1 ? pl.cta_seg[cls][cta] - 1 : 0;
+        s = p < p1 ? pl.run_seg[CLS][worker] - 1 : 0;
         g.a = 0;
         g.ntiles = 0;
         ntiles = 0;
     }
     __device__ __forceinline__ bool next(int hkv)
     {
+        constexpr int LEAD = attn_lead(CLS);
         p += ntiles;
         if (p >= p1)
             return false;
-        while (p >= g.a + (long long)g.ntiles * hkv)
+        while (g.ntiles == 0 || p >= g.a + (long long)(g.ntiles + LEAD) * hkv)
             g = seg[++s];
-        const long long o = p - g.a;
-        h = (int)(o / g.ntiles);
-        tile0 = (int)(o - (long long)h * g.ntiles);
+        int u;
+        h = div_units(p - g.a, g.ntiles + LEAD, u);
+        if (u < LEAD) {
+            p += LEAD - u;
+            if (p >= p1)
+                return false;
+            u = LEAD;
+        }
+        tile0 = u - LEAD;
         ntiles = (int)min((long long)(g.ntiles - tile0), p1 - p);
         return true;
     }

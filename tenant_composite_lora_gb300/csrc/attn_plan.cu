@@ -80,7 +80,7 @@ __device__ __forceinline__ int tile_keys(const Reader &r, int G, int rows, int k
     return max(0, min(r.len, r.t0 + last / G + r.lim));
 }
 
-// Block 0: the batch's row pointers and lengths, the segments and the CTAs'
+// Block 0: the batch's row pointers and lengths, the segments and the workers'
 // runs; the other blocks: the page tables, a warp per request or group.
 __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, const AttnPlanSrc s)
 {
@@ -107,15 +107,9 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
             p.hdr[AH_NREQ] = B;
             p.hdr[AH_NGRP] = NG;
         }
-        for (int t = tid; t < s.TQ; t += AP_THREADS)
-            p.tok_req[t] = B > 0 ? row_of(s.q_off, B, t) : -1;
-        for (int b = tid; b < B; b += AP_THREADS) {
-            p.q_off[b] = s.q_off[b];
-            p.grp[b] = NG > 0 ? row_of(s.g_off, NG, b) : -1;
-        }
         // the segments: groups, then requests
         const int G = p.hq / p.hkv;
-        long long segs[2] = {0, 0}, tiles[2] = {0, 0}, rows[2] = {0, 0};
+        long long segs[2] = {0, 0}, units_of[2] = {0, 0}, rows[2] = {0, 0};
         for (int i0 = 0; i0 < NG + B; i0 += AP_THREADS) {
             const int i = i0 + tid;
             Reader r{0, 0, 0, 0};
@@ -124,7 +118,6 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                 r.n = s.q_off[s.g_off[i + 1]] - r.t0;
                 r.len = checked_len(s.p_len[i], s.p_stride, p.page, status);
                 r.lim = 1 << 30;
-                p.g_row0[i] = r.t0;
             } else if (i < NG + B) {
                 const int b = i - NG;
                 r.t0 = s.q_off[b];
@@ -136,9 +129,11 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
             const int cls = all_rows > NA_ROWS ? AC_WIDE : AC_NARROW;
             const int tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS, tk = cls == AC_WIDE ? WA_KEYS : NA_KEYS;
             const int nt = (all_rows + tr - 1) / tr;
-            long long my_tiles = 0;
+            // (a tile whose rows see no key takes no units)
+            auto units = [&](int tiles) { return tiles > 0 ? tiles + attn_lead(cls) : 0; };
+            long long mine = 0;
             for (int k = 0; k < nt; ++k)
-                my_tiles += (tile_keys(r, G, tr, k) + tk - 1) / tk;
+                mine += units((tile_keys(r, G, tr, k) + tk - 1) / tk);
             long long seg0 = 0, a = 0, row = 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -146,8 +141,8 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                 const bool is = cls == c;
                 const long long s0 = segs[c] + block_before(is ? nt : 0, all, sh);
                 segs[c] += all;
-                const long long a0 = tiles[c] + p.hkv * block_before(is ? my_tiles : 0, all, sh);
-                tiles[c] += p.hkv * all;
+                const long long a0 = units_of[c] + p.hkv * block_before(is ? mine : 0, all, sh);
+                units_of[c] += p.hkv * all;
                 const long long row0 = rows[c] + p.hkv * block_before(is ? all_rows : 0, all, sh);
                 rows[c] += p.hkv * all;
                 if (is) {
@@ -171,21 +166,22 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                 g.src = i < NG ? ~i : i - NG;
                 g.lim = r.lim;
                 p.seg[cls][seg0 + k] = g;
-                a += (long long)p.hkv * g.ntiles;
+                a += (long long)p.hkv * units(g.ntiles);
                 row += (long long)p.hkv * g.nrows;
             }
         }
         __syncthreads();  // the segments are written (by this block)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const long long run = (tiles[c] + p.ctas[c] - 1) / p.ctas[c];
+            const int least = c == AC_WIDE ? WA_MIN_RUN : NA_MIN_RUN;
+            const long long run = max((long long)least, (units_of[c] + p.workers[c] - 1) / p.workers[c]);
             if (tid == 0) {
-                p.len[c * AL_WORDS + AL_TILES] = tiles[c];
+                p.len[c * AL_WORDS + AL_UNITS] = units_of[c];
                 p.len[c * AL_WORDS + AL_RUN] = run;
                 p.len[c * AL_WORDS + AL_PART] =
-                    c == AC_NARROW ? 0 : (long long)p.ctas[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
+                    c == AC_NARROW ? 0 : (long long)p.workers[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
             }
-            for (int x = tid; x < p.ctas[c]; x += AP_THREADS) {
+            for (int x = tid; x < p.workers[c]; x += AP_THREADS) {
                 const long long at = x * run;
                 int lo = 0, hi = (int)segs[c];  // last segment starting at or before `at`: the one that holds it
                 while (hi - lo > 1) {
@@ -195,8 +191,22 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                     else
                         hi = mid;
                 }
-                p.cta_seg[c][x] = lo;
+                p.run_seg[c][x] = lo;
             }
+        }
+        for (int t = tid; t < s.TQ; t += AP_THREADS) {
+            int4 k = make_int4(-1, 0, -1, 0);
+            if (B > 0) {
+                const int b = row_of(s.q_off, B, t);
+                k.z = p.sseg[b];
+                k.w = (t - s.q_off[b]) * G;
+                if (NG > 0) {
+                    const int g = row_of(s.g_off, NG, b);
+                    k.x = p.pseg[g];
+                    k.y = (t - s.q_off[s.g_off[g]]) * G;
+                }
+            }
+            p.tok[t] = k;
         }
         return;
     }
@@ -250,8 +260,8 @@ void free_plan(lora_attn_plan *p)
     if (!p)
         return;
     AttnPlanDev &d = p->dev;
-    void *all[] = {d.hdr,     d.len,    d.q_off,  d.grp,        d.g_row0,     d.tok_req, d.sseg,   d.pseg,
-                   d.s_pages, d.p_pages, d.seg[0], d.seg[1], d.cta_seg[0], d.cta_seg[1], d.part,    d.part_ml};
+    void *all[] = {d.hdr,    d.len,    d.sseg,       d.pseg,       d.tok,  d.s_pages, d.p_pages,
+                   d.seg[0], d.seg[1], d.run_seg[0], d.run_seg[1], d.part, d.part_ml};
     for (void *x : all)
         if (x)
             cudaFree(x);
@@ -301,35 +311,32 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     d.d = head_dim;
     d.page = page_size;
     d.page_log2 = __builtin_ctz((unsigned)page_size);
-    d.ctas[AC_NARROW] = NA_CTAS_PER_SM * sm_count();
-    d.ctas[AC_WIDE] = sm_count();
+    d.workers[AC_NARROW] = NA_WARPS * NA_CTAS_PER_SM * sm_count();
+    d.workers[AC_WIDE] = sm_count();
     // a row tile of every group and request and one per full tile of rows;
     // a query row has partial rows for the prefix and the request's own
-    // tokens, and each end of a CTA's run splits one row tile
+    // tokens, and each end of a worker's run splits one row tile
     const long long tokens_rows = (long long)max_queries * (n_q_heads / n_kv_heads);
     const long long segs = (long long)max_groups + max_requests + 2 * (tokens_rows / WA_ROWS + 1);
     d.pitch[AC_NARROW] = NA_ROWS;
     d.pitch[AC_WIDE] = (int)(tokens_rows < WA_ROWS ? tokens_rows : WA_ROWS);
-    const long long part_rows = (long long)d.ctas[AC_NARROW] * d.pitch[AC_NARROW] +
-                                (long long)d.ctas[AC_WIDE] * d.pitch[AC_WIDE] + 2ll * max_queries * n_q_heads;
+    const long long part_rows = (long long)d.workers[AC_NARROW] * d.pitch[AC_NARROW] +
+                                (long long)d.workers[AC_WIDE] * d.pitch[AC_WIDE] + 2ll * max_queries * n_q_heads;
     if (segs > 0x7fffffffll || tokens_rows > 0x3fffffffll) {
         free_plan(p);
         return LORA_ERR_NOT_SUPPORTED;
     }
     d.max_segs = (int)segs;
     cudaError_t e = plan_alloc(&d.hdr, AH_WORDS);
-    if (e == cudaSuccess) e = plan_alloc(&d.q_off, (size_t)max_requests + 1);
     if (e == cudaSuccess) e = plan_alloc(&d.len, AL_WORDS);
-    if (e == cudaSuccess) e = plan_alloc(&d.grp, (size_t)max_requests);
-    if (e == cudaSuccess) e = plan_alloc(&d.g_row0, (size_t)max_groups);
     if (e == cudaSuccess) e = plan_alloc(&d.sseg, (size_t)max_requests);
     if (e == cudaSuccess) e = plan_alloc(&d.pseg, (size_t)max_groups);
-    if (e == cudaSuccess) e = plan_alloc(&d.tok_req, (size_t)max_queries);
+    if (e == cudaSuccess) e = plan_alloc(&d.tok, (size_t)max_queries);
     if (e == cudaSuccess) e = plan_alloc(&d.s_pages, (size_t)max_requests * max_suffix_pages);
     if (e == cudaSuccess) e = plan_alloc(&d.p_pages, (size_t)max_groups * max_prefix_pages);
     for (int c = 0; c < 2; ++c) {
         if (e == cudaSuccess) e = plan_alloc(&d.seg[c], (size_t)segs);
-        if (e == cudaSuccess) e = plan_alloc(&d.cta_seg[c], (size_t)d.ctas[c]);
+        if (e == cudaSuccess) e = plan_alloc(&d.run_seg[c], (size_t)d.workers[c]);
     }
     if (e == cudaSuccess) e = plan_alloc(&d.part, (size_t)part_rows * head_dim);
     if (e == cudaSuccess) e = plan_alloc(&d.part_ml, (size_t)part_rows);

@@ -5,6 +5,7 @@
 // A CTA per SM walks its run of (256 rows x 128 keys) tiles:
 //  * warp 8 brings the tiles' keys and values, page by page, by TMA through a
 //    ring of 32 KB slots (keys, values, keys, ... in turn);
+//  * warps 10 and 11 gather a piece's queries while the piece before ends;
 //  * warp 9 (one thread) issues the products: S = Q K^T of both 128-row
 //    halves into tensor memory, later O += P V with P read from tensor
 //    memory, where it replaces S;
@@ -19,6 +20,8 @@
 //
 // Bound, from 128 rows up, by the products (4 of 128 x 128 x D a tile) and
 // the exponentials (256 x 128 a tile) about alike; below by the cache's bytes.
+#include <cstring>
+
 #include "attn_core.cuh"
 
 namespace tcl {
@@ -26,7 +29,8 @@ namespace tcl {
 namespace {
 
 constexpr int WA_SOFT = 256;                // warps 0-7: a row each
-constexpr int WA_THREADS = WA_SOFT + 128;   // warp 8: TMA; warp 9: MMA; a whole warpgroup, for the register split
+constexpr int WA_THREADS = WA_SOFT + 128;   // warp 8: TMA; warp 9: MMA; warps 10, 11: queries
+constexpr int WA_LOADERS = 64;
 constexpr int WA_HALF = 128;                // rows of one product
 constexpr float WA_SLACK = 8.f;
 // Registers: 384 threads are launched with 168 each (64,512 in all); the rows' warps take 216, the others 72.
@@ -47,7 +51,7 @@ static_assert(WaShape<128>::SMEM + 256 <= 232448 && WaShape<64>::SMEM + 256 <= 2
 
 struct WaBars {
     uint64_t full[8], empty[8];      // ring slots
-    uint64_t q_full[2];              // a half's queries are in shared memory
+    uint64_t q_full[2], q_free[2];   // a half's queries are in shared memory; their last product has ended
     uint64_t s_full[2], p_full[2];   // its S is computed; its P is written
     uint64_t pv_done[2];             // its O holds this tile
     uint64_t drain;                  // all products issued have ended
@@ -72,7 +76,7 @@ __device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
     const bool mine = lane < per;
     int it = 0;  // slots filled
     bool ok = true;
-    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    PieceWalk<AC_WIDE> w(p, blockIdx.x);
     while (ok && w.next(p.hkv)) {
         const int32_t *pages = pages_of(p, w.g.src);
         const int nkeys = w.g.nkeys;
@@ -86,7 +90,7 @@ __device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
             const int row = page < 0 ? oob_row : (page * p.hkv + w.h) * p.page + (key & (p.page - 1));
             for (int side = 0; side < 2; ++side, ++it) {
                 const int s = it % S::SLOTS;
-                if (it >= S::SLOTS && !mbar_wait_bounded(&bar.empty[s], ((it / S::SLOTS) - 1) & 1, status)) {
+                if (it >= S::SLOTS && !mbar_wait_now(&bar.empty[s], ((it / S::SLOTS) - 1) & 1, status)) {
                     ok = false;
                     break;
                 }
@@ -103,7 +107,50 @@ __device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
     }
     // every load has landed before the CTA can exit
     for (int i = max(0, it - S::SLOTS); i < it && ok; ++i)
-        ok = mbar_wait_bounded(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status);
+        ok = mbar_wait_now(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status);
+}
+
+// ---- the queries' warps: a piece's rows, gathered into the product's operand layout
+template <int D>
+__device__ void wa_queries(const AttnPlanDev &p, const AttnArgs &a, unsigned char *qsm, WaBars &bar)
+{
+    constexpr int CH = D / 8, STEP = WA_LOADERS / CH;  // 16-byte chunks of a row; rows between a thread's
+    const int i = threadIdx.x - (WA_THREADS - WA_LOADERS), ch = i % CH;
+    int32_t *status = p.hdr + AH_STATUS;
+    const int G = p.hq / p.hkv;
+    // the weights 2^(s c - m) want c > 0: a negative scale turns the queries' signs, a scale of 0 makes them 0
+    const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u, q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    int n[2] = {0, 0};
+    PieceWalk<AC_WIDE> w(p, blockIdx.x);
+    while (w.next(p.hkv)) {
+        const AttnSeg &g = w.g;
+        for (int half = 0; half < 2 && half * WA_HALF < g.nrows; ++half) {
+            if (n[half] > 0 && !mbar_wait_now(&bar.q_free[half], (n[half] - 1) & 1, status))
+                return;
+            ++n[half];
+            unsigned char *dst = qsm + half * (WA_HALF * D * 2);
+            int gr = g.row0 + half * WA_HALF + i / CH, t = gr / G, head = gr - t * G;
+            for (int row = i / CH; row < WA_HALF; row += STEP) {
+                unsigned char *d = dst + sw128_offset(row, ch * 8, WA_HALF);
+                if (half * WA_HALF + row < g.nrows)
+                    cp_async16(d, a.q + t * a.q_stride + (long long)(w.h * G + head) * D + ch * 8);
+                else
+                    *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
+                for (head += STEP; head >= G; head -= G)
+                    ++t;
+            }
+            cp_async_wait_all();
+            if (~q_and | q_xor)
+                for (int row = i / CH; row < WA_HALF; row += STEP) {
+                    uint4 *d = reinterpret_cast<uint4 *>(dst + sw128_offset(row, ch * 8, WA_HALF));
+                    const uint4 x = *d;
+                    *d = make_uint4((x.x & q_and) ^ q_xor, (x.y & q_and) ^ q_xor, (x.z & q_and) ^ q_xor,
+                                    (x.w & q_and) ^ q_xor);
+                }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar.q_full[half]);
+        }
+    }
 }
 
 // ---- MMA thread
@@ -117,7 +164,7 @@ __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars 
     const uint32_t id_pv = umma_idesc_bf16(WA_HALF, D) | (1u << 16);  // B = V: MN-major
     int it = 0;  // slots consumed
     int nq[2] = {0, 0}, np[2] = {0, 0};
-    auto scores = [&](int q, uint32_t k) {  // S_q = Q_q K^T
+    auto scores = [&](int q, uint32_t k, bool last) {  // S_q = Q_q K^T; last: of the piece
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (uint32_t)(kk >> 2) * (WA_HALF * 128) + (kk & 3) * 32;
@@ -125,18 +172,20 @@ __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars 
                       umma_desc_sw128(k + off), id_qk, kk > 0);
         }
         umma_commit(&bar.s_full[q]);
+        if (last)
+            umma_commit(&bar.q_free[q]);
     };
-    auto slot_full = [&](int i) { return mbar_wait_bounded(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status); };
+    auto slot_full = [&](int i) { return mbar_wait_now(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status); };
     bool ok = true;
-    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    PieceWalk<AC_WIDE> w(p, blockIdx.x);
     while (ok && w.next(p.hkv)) {
         const int halves = w.g.nrows > WA_HALF ? 2 : 1;
         ok = slot_full(it);
         for (int q = 0; ok && q < halves; ++q) {
-            ok = mbar_wait_bounded(&bar.q_full[q], nq[q]++ & 1, status);
+            ok = mbar_wait_now(&bar.q_full[q], nq[q]++ & 1, status);
             tc_fence_after();
             if (ok)
-                scores(q, ring + (it % S::SLOTS) * S::SLOT);
+                scores(q, ring + (it % S::SLOTS) * S::SLOT, w.ntiles == 1);
         }
         if (!ok)
             break;
@@ -146,9 +195,9 @@ __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars 
             // now: it = this tile's values, it + 1 = the next tile's keys
             const bool more = k + 1 < w.ntiles;
             const uint32_t v = ring + (it % S::SLOTS) * S::SLOT, kn = ring + ((it + 1) % S::SLOTS) * S::SLOT;
-            ok = slot_full(it) && (!more || slot_full(it + 1));
+            ok = slot_full(it);
             for (int q = 0; ok && q < halves; ++q) {
-                ok = mbar_wait_bounded(&bar.p_full[q], np[q] & 1, status);
+                ok = mbar_wait_now(&bar.p_full[q], np[q] & 1, status);
                 if (!ok)
                     break;
                 ++np[q];
@@ -158,8 +207,12 @@ __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars 
                     umma_bf16_ta(t + S::O0 + q * D, t + S::S0 + q * 128 + kk * 8,
                                  umma_desc_sw128_mn(v + kk * 2048, WA_KEYS * 128, 1024), id_pv, k > 0 || kk > 0);
                 umma_commit(&bar.pv_done[q]);
-                if (more)
-                    scores(q, kn);
+                if (more) {
+                    ok = q > 0 || slot_full(it + 1);
+                    if (!ok)
+                        break;
+                    scores(q, kn, k + 2 == w.ntiles);
+                }
             }
             if (!ok)
                 break;
@@ -172,13 +225,37 @@ __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars 
         }
     }
     umma_commit(&bar.drain);
-    mbar_wait_bounded(&bar.drain, 0, status);
+    mbar_wait_now(&bar.drain, 0, status);
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
 }
 
 // ---- softmax warps: thread = row
 template <int D>
-__device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_bfloat16 *vcache, unsigned char *qsm,
-                           unsigned char *ring, WaBars &bar)
+__device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_bfloat16 *vcache, unsigned char *ring,
+                           WaBars &bar)
 {
     typedef WaShape<D> S;
     const int tid = threadIdx.x, half = tid >> 7, r = tid & 127, lane = tid & 31;
@@ -187,36 +264,15 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
     const bool bad_pages = (*(volatile int32_t *)status & LORA_DEV_BAD_PAGE) != 0;
     const uint32_t quarter = (uint32_t)((r >> 5) * 32) << 16;  // this warp's tensor memory lanes
     const uint32_t ts = bar.taddr + quarter + S::S0 + half * 128, to = bar.taddr + quarter + S::O0 + half * D;
-    // 2^(s * c - m) wants c > 0: a negative scale turns the queries' signs, a scale of 0 makes them 0
-    const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
-    const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u, q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);  // (see wa_queries)
     int nt = 0;    // tiles of this half so far
     int it = 0;    // ring slots so far
     // once a wait has run out (ok is the same in all lanes of a warp) only the barriers are still met
     bool ok = true;
-    PieceWalk w(p, AC_WIDE, blockIdx.x);
+    PieceWalk<AC_WIDE> w(p, blockIdx.x);
     while (w.next(p.hkv)) {
         const AttnSeg &g = w.g;
-        const bool active = half * WA_HALF < g.nrows;
-        if (active) {
-            // this half's queries; the products that read the ones before have ended (their S was waited for)
-            for (int i = r; i < WA_HALF * (D / 8); i += 128) {
-                const int row = i / (D / 8), ch = i % (D / 8), rr = half * WA_HALF + row;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (rr < g.nrows) {
-                    const int gr = g.row0 + rr, t = gr / G;
-                    x = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (long long)(w.h * G + gr % G) * D +
-                                                         ch * 8);
-                    x.x = (x.x & q_and) ^ q_xor;
-                    x.y = (x.y & q_and) ^ q_xor;
-                    x.z = (x.z & q_and) ^ q_xor;
-                    x.w = (x.w & q_and) ^ q_xor;
-                }
-                *reinterpret_cast<uint4 *>(qsm + half * (WA_HALF * D * 2) + sw128_offset(row, ch * 8, WA_HALF)) = x;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar.q_full[half]);
-        } else {
+        if (half * WA_HALF >= g.nrows) {
             it += 2 * w.ntiles;
             continue;
         }
@@ -233,7 +289,7 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
         }
         float m = -INFINITY, l = 0.f;
         for (int k = 0; ok && k < w.ntiles; ++k, ++nt, it += 2) {
-            ok = mbar_wait_bounded(&bar.s_full[half], nt & 1, status);
+            ok = mbar_wait_now(&bar.s_full[half], nt & 1, status);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -265,8 +321,9 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-                mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
+            for (int i = 0; i < 128; i += 2)
+                mx[(i >> 1) & 3] = fmaxf(fmaxf(mx[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31])),
+                                         __uint_as_float(s[i >> 5][(i + 1) & 31]));
             const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
             if (k == 0) {
                 m = mnew;
@@ -275,7 +332,7 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
                 const float f = m == mnew ? 1.f : pow2(m - mnew);
                 m = mnew;
                 l *= f;
-                ok = mbar_wait_bounded(&bar.pv_done[half], (nt - 1) & 1, status);
+                ok = mbar_wait_now(&bar.pv_done[half], (nt - 1) & 1, status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -294,26 +351,33 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
                 }
             }
             const float nb = m == -INFINITY ? 0.f : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t cc = pair(c, c), bb = pair(nb, nb);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t pk[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float x = pow2(fmaf(__uint_as_float(s[2 * i + (j >> 4)][(2 * j) & 31]), c, nb));
-                    const float y = pow2(fmaf(__uint_as_float(s[2 * i + (j >> 4)][(2 * j + 1) & 31]), c, nb));
-                    sum[(2 * j) & 3] += x;
-                    sum[(2 * j + 1) & 3] += y;
+                    float x, y;
+                    unpair(fma2(pair(__uint_as_float(s[2 * i + (j >> 4)][(2 * j) & 31]),
+                                     __uint_as_float(s[2 * i + (j >> 4)][(2 * j + 1) & 31])),
+                                cc, bb),
+                           x, y);
+                    x = pow2(x);
+                    y = pow2(y);
+                    sum[j & 1] = add2(sum[j & 1], pair(x, y));
                     pk[j] = pack_bf16(x, y);
                 }
                 tmem_st32(ts + i * 32, pk);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float l0, l1;
+            unpair(add2(sum[0], sum[1]), l0, l1);
+            l += l0 + l1;
             // the first half sees to the values: beyond the keys they count as 0, whatever they hold; one that is
             // not finite and that only some rows see is taken out here and added to those rows at the end
             if (half == 0 && key0 + WA_KEYS > lim_first) {
                 const int vs = it + 1;
-                ok = mbar_wait_bounded(&bar.full[vs % S::SLOTS], (vs / S::SLOTS) & 1, status);
+                ok = mbar_wait_now(&bar.full[vs % S::SLOTS], (vs / S::SLOTS) & 1, status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -352,7 +416,7 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
             mbar_arrive(&bar.p_full[half]);
         }
         // the piece's result
-        ok = ok && mbar_wait_bounded(&bar.pv_done[half], (nt - 1) & 1, status);
+        ok = ok && mbar_wait_now(&bar.pv_done[half], (nt - 1) & 1, status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         bool poison = false;
@@ -421,7 +485,8 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
             mbar_init(&bar.empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) {
-            mbar_init(&bar.q_full[q], 128);
+            mbar_init(&bar.q_full[q], WA_LOADERS);
+            mbar_init(&bar.q_free[q], 1);
             mbar_init(&bar.s_full[q], 1);
             mbar_init(&bar.p_full[q], 128);
             mbar_init(&bar.pv_done[q], 1);
@@ -438,12 +503,14 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
     pdl_launch_dependents();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WA_REGS_ROWS));
-        wa_softmax<D>(p, a, vcache, smem, smem + S::Q, bar);
+        wa_softmax<D>(p, a, vcache, smem + S::Q, bar);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WA_REGS_REST));
         if (warp == 8)
             wa_produce<D>(mk, mv, p, a.oob_row, smem + S::Q, bar);
-        else if (warp == 9 && lane == 0)
+        else if (warp >= 10)
+            wa_queries<D>(p, a, smem, bar);
+        else if (lane == 0)
             wa_mma<D>(p, smem_u32(smem), smem_u32(smem + S::Q), bar);
     }
     __syncwarp();
@@ -455,8 +522,7 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
 }
 
 template <int D>
-cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                     const __nv_bfloat16 *vcache, cudaStream_t st)
+cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)
 {
     static thread_local int attr_dev = -1;  // per host thread
     int dev = 0;
@@ -468,15 +534,18 @@ cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap 
             return e;
         attr_dev = dev;
     }
-    return launch_pdl(k_attn_wide<D>, dim3(p.ctas[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, p, a, vcache);
+    CUtensorMap mk, mv;
+    std::memcpy(&mk, cache.map_k[AC_WIDE], sizeof(mk));
+    std::memcpy(&mv, cache.map_v[AC_WIDE], sizeof(mv));
+    const __nv_bfloat16 *v = cache.v;
+    return launch_pdl(k_attn_wide<D>, dim3(p.workers[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, p, a, v);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                             const __nv_bfloat16 *vcache, cudaStream_t st)
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)
 {
-    return p.d == 64 ? run_wide<64>(p, a, mk, mv, vcache, st) : run_wide<128>(p, a, mk, mv, vcache, st);
+    return p.d == 64 ? run_wide<64>(p, a, cache, st) : run_wide<128>(p, a, cache, st);
 }
 
 }  // namespace tcl

@@ -151,11 +151,13 @@ lora_status lora_kv_cache_create(int num_pages, int page_size, int n_kv_heads, i
     c->d = head_dim;
     c->k = static_cast<__nv_bfloat16 *>(k_dev);
     c->v = static_cast<__nv_bfloat16 *>(v_dev);
-    // the attention's loads: one head's rows of a page, at most 64 at a time
     const long long rows = (long long)num_pages * n_kv_heads * page_size;
-    const int box = page_size < ATTN_BOX_MAX ? page_size : ATTN_BOX_MAX;
-    c->maps_ready = encode_kv_rows(c->map_k, k_dev, head_dim, rows, box) == cudaSuccess &&
-                    encode_kv_rows(c->map_v, v_dev, head_dim, rows, box) == cudaSuccess;
+    c->maps_ready = true;
+    for (int cls = 0; cls < 2; ++cls) {
+        const int box = cls == AC_NARROW ? NA_KEYS : page_size < ATTN_BOX_MAX ? page_size : ATTN_BOX_MAX;
+        c->maps_ready = c->maps_ready && encode_kv_rows(c->map_k[cls], k_dev, head_dim, rows, box) == cudaSuccess &&
+                        encode_kv_rows(c->map_v[cls], v_dev, head_dim, rows, box) == cudaSuccess;
+    }
     *out = c;
     return LORA_OK;
 }
