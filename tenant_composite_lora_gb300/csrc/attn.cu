@@ -350,85 +350,76 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
 
 // ---------------------------------------------------------------- combine
 
-// W warps per (query token, head): its pieces of the prefix, then of the
-// request's own tokens, in the order of the keys, an equal share per warp.
-// Few rows (at most CB_FEW) take eight warps each, as their keys are cut into
-// many pieces; more rows fill the SMs with one.
 constexpr int CB_BATCH = 4;  // pieces whose sums are on their way at a time
 
-template <int D, int W>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) k_attn_combine(const AttnPlanDev p, const AttnArgs a)
+// The pieces of one query row and head: of the prefix, then of the request's
+// own tokens, in the order of the keys.
+struct RowPieces {
+    long long base[2];
+    int n[2], pitch[2];
+    __device__ __forceinline__ void find(const AttnPlanDev &p, const int4 &tok, int h, int g)
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int code = k ? tok.z : tok.x, r = (k ? tok.w : tok.y) + g;
+            n[k] = 0;
+            base[k] = 0;
+            pitch[k] = 0;
+            if (code < 0)
+                continue;
+            const int cls = code & 1, tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS, lead = attn_lead(cls);
+            const long long *len = p.len + cls * AL_WORDS;
+            const AttnSeg &s = p.seg[cls][(code >> 1) + r / tr];
+            if (s.ntiles == 0)
+                continue;
+            const long long a0 = s.a + (long long)h * (s.ntiles + lead) + lead, run = len[AL_RUN];
+            int c0, c1, rem;
+            if (run >> 31) {
+                c0 = (int)(a0 / run);
+                c1 = (int)((a0 + s.ntiles - 1) / run);
+            } else {
+                c0 = div_units(a0, (int)run, rem);
+                c1 = div_units(a0 + s.ntiles - 1, (int)run, rem);
+            }
+            n[k] = c1 - c0 + 1;
+            pitch[k] = p.pitch[cls];
+            base[k] = len[AL_PART] + (long long)c0 * pitch[k] + s.rows0 + (long long)h * s.nrows + r % tr;
+        }
+    }
+    __device__ __forceinline__ long long at(int i) const
+    {
+        return i < n[0] ? base[0] + (long long)i * pitch[0] : base[1] + (long long)(i - n[0]) * pitch[1];
+    }
+};
+
+// Joins pieces i0 .. i1 of a row relative to the maximum B: its sums (D / 32
+// elements a lane) and L.
+template <int D>
+__device__ __forceinline__ void join(const AttnPlanDev &p, const RowPieces &rp, int i0, int i1, float B, int lane,
+                                     float (&acc)[D / 32], float &L)
 {
     constexpr int E = D / 32;
-    __shared__ float s_acc[W][D];
-    __shared__ float s_l[W];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = W == 1 ? (long long)blockIdx.x * 4 + warp : blockIdx.x;
-    const int part = W == 1 ? 0 : warp;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (row >= (long long)a.TQ * p.hq)
-        return;
-    const int t = (int)(row / p.hq), hq = (int)(row % p.hq), G = p.hq / p.hkv, h = hq / G;
-    const int4 tok = p.tok[t];
-    long long base[2] = {0, 0};
-    int pitch[2] = {0, 0}, n[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int code = k ? tok.z : tok.x, r = (k ? tok.w : tok.y) + hq % G;
-        if (code < 0)
-            continue;
-        const int cls = code & 1, tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS, lead = attn_lead(cls);
-        const long long *len = p.len + cls * AL_WORDS;
-        const AttnSeg &g = p.seg[cls][(code >> 1) + r / tr];
-        if (g.ntiles == 0)
-            continue;
-        const long long a0 = g.a + (long long)h * (g.ntiles + lead) + lead, run = len[AL_RUN];
-        int c0, c1, rem;
-        if (run >> 31) {
-            c0 = (int)(a0 / run);
-            c1 = (int)((a0 + g.ntiles - 1) / run);
-        } else {
-            c0 = div_units(a0, (int)run, rem);
-            c1 = div_units(a0 + g.ntiles - 1, (int)run, rem);
-        }
-        n[k] = c1 - c0 + 1;
-        pitch[k] = p.pitch[cls];
-        base[k] = len[AL_PART] + (long long)c0 * pitch[k] + g.rows0 + (long long)h * g.nrows + r % tr;
-    }
-    auto part_row = [&](int i) {
-        return i < n[0] ? base[0] + (long long)i * pitch[0] : base[1] + (long long)(i - n[0]) * pitch[1];
-    };
-    const int np = n[0] + n[1];
-    float M = -INFINITY;
-    for (int i = lane; i < np; i += 32)
-        M = fmaxf(M, p.part_ml[part_row(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float B = M == -INFINITY ? 0.f : M;
-    float acc[E] = {}, L = 0.f;
-    const int i0 = part * np / W, i1 = (part + 1) * np / W;
     for (int i = i0; i < i1; i += CB_BATCH) {
         float2 ml[CB_BATCH];
         float v[CB_BATCH][E];
 #pragma unroll
-        for (int j = 0; j < CB_BATCH; ++j) {
-            const long long pr = part_row(min(i + j, i1 - 1));
-            ml[j] = p.part_ml[pr];
-            const float *x = p.part + pr * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(x);
-                v[j][0] = y.x;
-                v[j][1] = y.y;
-                v[j][2] = y.z;
-                v[j][3] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2 *>(x);
-                v[j][0] = y.x;
-                v[j][1] = y.y;
+        for (int j = 0; j < CB_BATCH; ++j)
+            if (i + j < i1) {
+                const long long pr = rp.at(i + j);
+                ml[j] = p.part_ml[pr];
+                const float *x = p.part + pr * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(x);
+                    v[j][0] = y.x;
+                    v[j][1] = y.y;
+                    v[j][2] = y.z;
+                    v[j][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(x);
+                    v[j][0] = y.x;
+                    v[j][1] = y.y;
+                }
             }
-        }
 #pragma unroll
         for (int j = 0; j < CB_BATCH; ++j)
             if (i + j < i1) {
@@ -439,22 +430,24 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32) k_attn_combine(const At
                     acc[e] += f * v[j][e];
             }
     }
-    if constexpr (W > 1) {
+}
+
+__device__ __forceinline__ float row_max(const AttnPlanDev &p, const RowPieces &rp, int np, int lane)
+{
+    float M = -INFINITY;
+    for (int i = lane; i < np; i += 32)
+        M = fmaxf(M, p.part_ml[rp.at(i)].x);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            s_acc[warp][lane * E + e] = acc[e];
-        if (lane == 0)
-            s_l[warp] = L;
-        __syncthreads();
-        if (warp > 0)
-            return;
-        for (int v = 1; v < W; ++v) {
-            L += s_l[v];
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] += s_acc[v][lane * E + e];
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    return M;
+}
+
+template <int D>
+__device__ __forceinline__ void write_row(const AttnArgs &a, int hq_all, int t, int hq, const float (&acc)[D / 32],
+                                          float M, float L, int lane)
+{
+    constexpr int E = D / 32;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     __nv_bfloat16 *o = a.out + t * a.out_stride + (long long)hq * D + lane * E;
     if constexpr (E == 4)
@@ -463,7 +456,74 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32) k_attn_combine(const At
     else
         *reinterpret_cast<uint32_t *>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
     if (a.lse && lane == 0)
-        a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945f;
+        a.lse[(long long)t * hq_all + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945f;
+}
+
+// Many rows: a warp per (query token, key/value head) takes its query heads
+// in turn; where their pieces lie is looked up once for a row tile.
+template <int D>
+__global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const AttnArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (item >= (long long)a.TQ * p.hkv)
+        return;
+    const int t = (int)(item / p.hkv), h = (int)(item % p.hkv), G = p.hq / p.hkv;
+    const int4 tok = p.tok[t];
+    RowPieces rp;
+    for (int g = 0; g < G; ++g) {
+        // (a token's heads may lie in two tiles; 16 divides both classes' rows)
+        if (g == 0 || (tok.y + g) % NA_ROWS == 0 || (tok.w + g) % NA_ROWS == 0) {
+            rp.find(p, tok, h, g);
+        } else {
+            ++rp.base[0];
+            ++rp.base[1];
+        }
+        const int np = rp.n[0] + rp.n[1];
+        const float M = row_max(p, rp, np, lane);
+        float acc[D / 32] = {}, L = 0.f;
+        join<D>(p, rp, 0, np, M == -INFINITY ? 0.f : M, lane, acc, L);
+        write_row<D>(a, p.hq, t, h * G + g, acc, M, L, lane);
+    }
+}
+
+// Few rows, whose keys are cut into many pieces: eight warps a row, an equal
+// share of its pieces each.
+constexpr int CB_WARPS = 8;
+
+template <int D>
+__global__ void __launch_bounds__(CB_WARPS * 32) k_attn_combine_few(const AttnPlanDev p, const AttnArgs a)
+{
+    __shared__ float s_acc[CB_WARPS][D];
+    __shared__ float s_l[CB_WARPS];
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int t = blockIdx.x / p.hq, hq = blockIdx.x % p.hq, G = p.hq / p.hkv;
+    RowPieces rp;
+    rp.find(p, p.tok[t], hq / G, hq % G);
+    const int np = rp.n[0] + rp.n[1];
+    const float M = row_max(p, rp, np, lane);
+    float acc[E] = {}, L = 0.f;
+    join<D>(p, rp, warp * np / CB_WARPS, (warp + 1) * np / CB_WARPS, M == -INFINITY ? 0.f : M, lane, acc, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0)
+        s_l[warp] = L;
+    __syncthreads();
+    if (warp > 0)
+        return;
+    for (int v = 1; v < CB_WARPS; ++v) {
+        L += s_l[v];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] += s_acc[v][lane * E + e];
+    }
+    write_row<D>(a, p.hq, t, hq, acc, M, L, lane);
 }
 
 constexpr int CB_FEW = 1216;  // rows: eight warps an SM of 152 at one warp a row
@@ -502,8 +562,9 @@ cudaError_t run_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cach
         return e;
     const long long rows = (long long)a.TQ * p.hq;
     if (rows <= CB_FEW)
-        return launch_pdl(k_attn_combine<D, 8>, dim3((unsigned)rows), 256, 0, st, p, a);
-    return launch_pdl(k_attn_combine<D, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p, a);
+        return launch_pdl(k_attn_combine_few<D>, dim3((unsigned)rows), CB_WARPS * 32, 0, st, p, a);
+    const long long items = (long long)a.TQ * p.hkv;
+    return launch_pdl(k_attn_combine<D>, dim3((unsigned)((items + 3) / 4)), 128, 0, st, p, a);
 }
 
 }  // namespace

@@ -6,7 +6,7 @@
 //  * warp 8 brings the tiles' keys and values, page by page, by TMA through a
 //    ring of 32 KB slots (keys, values, keys, ... in turn);
 //  * warps 10 and 11 gather a piece's queries while the piece before ends;
-//  * warp 9 (one thread) issues the products: S = Q K^T of both 128-row
+//  * warp 9 issues the products: S = Q K^T of both 128-row
 //    halves into tensor memory, later O += P V with P read from tensor
 //    memory, where it replaces S;
 //  * warps 0-3 and 4-7 own a half each, a thread per row: S is read into
@@ -30,7 +30,6 @@ namespace {
 
 constexpr int WA_SOFT = 256;                // warps 0-7: a row each
 constexpr int WA_THREADS = WA_SOFT + 128;   // warp 8: TMA; warp 9: MMA; warps 10, 11: queries
-constexpr int WA_LOADERS = 64;
 constexpr int WA_HALF = 128;                // rows of one product
 constexpr float WA_SLACK = 8.f;
 // Registers: 384 threads are launched with 168 each (64,512 in all); the rows' warps take 216, the others 72.
@@ -110,121 +109,130 @@ __device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
         ok = mbar_wait_now(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status);
 }
 
-// ---- the queries' warps: a piece's rows, gathered into the product's operand layout
+// ---- the queries' warps: a half each of a piece's rows, gathered into the product's operand layout
 template <int D>
-__device__ void wa_queries(const AttnPlanDev &p, const AttnArgs &a, unsigned char *qsm, WaBars &bar)
+__device__ void wa_queries(const AttnPlanDev &p, const AttnArgs &a, unsigned char *qsm, WaBars &bar, int half)
 {
-    constexpr int CH = D / 8, STEP = WA_LOADERS / CH;  // 16-byte chunks of a row; rows between a thread's
-    const int i = threadIdx.x - (WA_THREADS - WA_LOADERS), ch = i % CH;
+    constexpr int CH = D / 8, STEP = 32 / CH;  // 16-byte chunks of a row; rows between a lane's
+    const int lane = threadIdx.x & 31, ch = lane % CH, first = half * WA_HALF + lane / CH;
     int32_t *status = p.hdr + AH_STATUS;
     const int G = p.hq / p.hkv;
     // the weights 2^(s c - m) want c > 0: a negative scale turns the queries' signs, a scale of 0 makes them 0
     const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u, q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    int n[2] = {0, 0};
+    unsigned char *dst = qsm + half * (WA_HALF * D * 2);
+    int n = 0;
     PieceWalk<AC_WIDE> w(p, blockIdx.x);
     while (w.next(p.hkv)) {
         const AttnSeg &g = w.g;
-        for (int half = 0; half < 2 && half * WA_HALF < g.nrows; ++half) {
-            if (n[half] > 0 && !mbar_wait_now(&bar.q_free[half], (n[half] - 1) & 1, status))
-                return;
-            ++n[half];
-            unsigned char *dst = qsm + half * (WA_HALF * D * 2);
-            int gr = g.row0 + half * WA_HALF + i / CH, t = gr / G, head = gr - t * G;
-            for (int row = i / CH; row < WA_HALF; row += STEP) {
-                unsigned char *d = dst + sw128_offset(row, ch * 8, WA_HALF);
-                if (half * WA_HALF + row < g.nrows)
-                    cp_async16(d, a.q + t * a.q_stride + (long long)(w.h * G + head) * D + ch * 8);
-                else
-                    *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
-                for (head += STEP; head >= G; head -= G)
-                    ++t;
-            }
-            cp_async_wait_all();
-            if (~q_and | q_xor)
-                for (int row = i / CH; row < WA_HALF; row += STEP) {
-                    uint4 *d = reinterpret_cast<uint4 *>(dst + sw128_offset(row, ch * 8, WA_HALF));
-                    const uint4 x = *d;
-                    *d = make_uint4((x.x & q_and) ^ q_xor, (x.y & q_and) ^ q_xor, (x.z & q_and) ^ q_xor,
-                                    (x.w & q_and) ^ q_xor);
-                }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar.q_full[half]);
+        if (half * WA_HALF >= g.nrows)
+            continue;
+        if (n > 0 && !mbar_wait_now(&bar.q_free[half], (n - 1) & 1, status))
+            return;
+        ++n;
+#pragma unroll 8
+        for (int i = 0; i < WA_HALF; i += STEP) {
+            const int row = first + i, gr = g.row0 + row, t = (unsigned)gr / (unsigned)G;
+            unsigned char *d = dst + sw128_offset(row - half * WA_HALF, ch * 8, WA_HALF);
+            if (row < g.nrows)
+                cp_async16(d, a.q + t * a.q_stride + (long long)(w.h * G + gr - t * G) * D + ch * 8);
+            else
+                *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
         }
+        cp_async_wait_all();
+        if (~q_and | q_xor)
+            for (int i = 0; i < WA_HALF; i += STEP) {
+                uint4 *d = reinterpret_cast<uint4 *>(dst + sw128_offset(lane / CH + i, ch * 8, WA_HALF));
+                const uint4 x = *d;
+                *d = make_uint4((x.x & q_and) ^ q_xor, (x.y & q_and) ^ q_xor, (x.z & q_and) ^ q_xor,
+                                (x.w & q_and) ^ q_xor);
+            }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar.q_full[half]);
     }
 }
 
-// ---- MMA thread
+// ---- MMA warp
 template <int D>
 __device__ void wa_mma(const AttnPlanDev &p, uint32_t qs, uint32_t ring, WaBars &bar)
 {
     typedef WaShape<D> S;
     int32_t *status = p.hdr + AH_STATUS;
-    const uint32_t t = bar.taddr;
+    const uint32_t t = __shfl_sync(0xffffffffu, bar.taddr, 0);
     const uint32_t id_qk = umma_idesc_bf16(WA_HALF, WA_KEYS);
     const uint32_t id_pv = umma_idesc_bf16(WA_HALF, D) | (1u << 16);  // B = V: MN-major
+    const bool leader = elect_one();
     int it = 0;  // slots consumed
     int nq[2] = {0, 0}, np[2] = {0, 0};
+    auto wait = [&](uint64_t *b, int n) { return __all_sync(0xffffffffu, mbar_wait_now(b, n & 1, status)) != 0; };
+    auto slot = [&](int i) { return __shfl_sync(0xffffffffu, ring + (i % S::SLOTS) * S::SLOT, 0); };
+    auto slot_full = [&](int i) { return wait(&bar.full[i % S::SLOTS], i / S::SLOTS); };
     auto scores = [&](int q, uint32_t k, bool last) {  // S_q = Q_q K^T; last: of the piece
+        // (a descriptor's start address counts 16-byte units: steps of 32 bytes, 16 KB a column block)
+        const uint64_t da = umma_desc_sw128(qs + q * (WA_HALF * D * 2)), db = umma_desc_sw128(k);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * (WA_HALF * 128) + (kk & 3) * 32;
-            umma_bf16(t + S::S0 + q * 128, umma_desc_sw128(qs + q * (WA_HALF * D * 2) + off),
-                      umma_desc_sw128(k + off), id_qk, kk > 0);
+            const uint32_t off = ((kk >> 2) * (WA_HALF * 128) + (kk & 3) * 32) >> 4;
+            umma_bf16_warp(t + S::S0 + q * 128, da + off, db + off, id_qk, kk > 0, leader);
         }
-        umma_commit(&bar.s_full[q]);
+        umma_commit_warp(&bar.s_full[q], leader);
         if (last)
-            umma_commit(&bar.q_free[q]);
+            umma_commit_warp(&bar.q_free[q], leader);
+        __syncwarp();
     };
-    auto slot_full = [&](int i) { return mbar_wait_now(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status); };
     bool ok = true;
     PieceWalk<AC_WIDE> w(p, blockIdx.x);
     while (ok && w.next(p.hkv)) {
         const int halves = w.g.nrows > WA_HALF ? 2 : 1;
         ok = slot_full(it);
-        for (int q = 0; ok && q < halves; ++q) {
-            ok = mbar_wait_now(&bar.q_full[q], nq[q]++ & 1, status);
-            tc_fence_after();
-            if (ok)
-                scores(q, ring + (it % S::SLOTS) * S::SLOT, w.ntiles == 1);
-        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (ok && q < halves) {
+                ok = wait(&bar.q_full[q], nq[q]++);
+                tc_fence_after();
+                if (ok)
+                    scores(q, slot(it), w.ntiles == 1);
+            }
         if (!ok)
             break;
-        umma_commit(&bar.empty[it % S::SLOTS]);
+        umma_commit_warp(&bar.empty[it % S::SLOTS], leader);
         ++it;
         for (int k = 0; ok && k < w.ntiles; ++k) {
             // now: it = this tile's values, it + 1 = the next tile's keys
             const bool more = k + 1 < w.ntiles;
-            const uint32_t v = ring + (it % S::SLOTS) * S::SLOT, kn = ring + ((it + 1) % S::SLOTS) * S::SLOT;
+            const uint64_t dv = umma_desc_sw128_mn(slot(it), WA_KEYS * 128, 1024);
+            const uint32_t kn = slot(it + 1);
             ok = slot_full(it);
-            for (int q = 0; ok && q < halves; ++q) {
-                ok = mbar_wait_now(&bar.p_full[q], np[q] & 1, status);
-                if (!ok)
-                    break;
-                ++np[q];
-                tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < WA_KEYS / 16; ++kk)
-                    umma_bf16_ta(t + S::O0 + q * D, t + S::S0 + q * 128 + kk * 8,
-                                 umma_desc_sw128_mn(v + kk * 2048, WA_KEYS * 128, 1024), id_pv, k > 0 || kk > 0);
-                umma_commit(&bar.pv_done[q]);
-                if (more) {
-                    ok = q > 0 || slot_full(it + 1);
+            for (int q = 0; q < 2; ++q)
+                if (ok && q < halves) {
+                    ok = wait(&bar.p_full[q], np[q]++);
                     if (!ok)
                         break;
-                    scores(q, kn, k + 2 == w.ntiles);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < WA_KEYS / 16; ++kk)
+                        umma_bf16_ta_warp(t + S::O0 + q * D, t + S::S0 + q * 128 + kk * 8, dv + kk * (2048 >> 4),
+                                          id_pv, k > 0 || kk > 0, leader);
+                    umma_commit_warp(&bar.pv_done[q], leader);
+                    if (more) {
+                        ok = q > 0 || slot_full(it + 1);
+                        if (!ok)
+                            break;
+                        scores(q, kn, k + 2 == w.ntiles);
+                    }
                 }
-            }
             if (!ok)
                 break;
-            umma_commit(&bar.empty[it % S::SLOTS]);
+            umma_commit_warp(&bar.empty[it % S::SLOTS], leader);
             ++it;
             if (more) {
-                umma_commit(&bar.empty[it % S::SLOTS]);
+                umma_commit_warp(&bar.empty[it % S::SLOTS], leader);
                 ++it;
             }
+            __syncwarp();
         }
     }
-    umma_commit(&bar.drain);
+    umma_commit_warp(&bar.drain, leader);
     mbar_wait_now(&bar.drain, 0, status);
 }
 
@@ -478,14 +486,14 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~static_cast<uintptr_t>(1023));
     __shared__ WaBars bar;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < S::SLOTS; ++s) {
             mbar_init(&bar.full[s], 1);
             mbar_init(&bar.empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) {
-            mbar_init(&bar.q_full[q], WA_LOADERS);
+            mbar_init(&bar.q_full[q], 32);
             mbar_init(&bar.q_free[q], 1);
             mbar_init(&bar.s_full[q], 1);
             mbar_init(&bar.p_full[q], 128);
@@ -509,8 +517,8 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
         if (warp == 8)
             wa_produce<D>(mk, mv, p, a.oob_row, smem + S::Q, bar);
         else if (warp >= 10)
-            wa_queries<D>(p, a, smem, bar);
-        else if (lane == 0)
+            wa_queries<D>(p, a, smem, bar, warp - 10);
+        else
             wa_mma<D>(p, smem_u32(smem), smem_u32(smem + S::Q), bar);
     }
     __syncwarp();
