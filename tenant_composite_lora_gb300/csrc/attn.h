@@ -99,6 +99,7 @@ struct AttnArgs {
     float scale_log2;  // scale / log 2: weights are powers of two
     int TQ, B;
     int oob_row;       // a row outside the cache: its loads give zeros
+    bool q_map;        // the wide kernel's queries come by TMA
 };
 cudaError_t launch_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
 cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);

@@ -4,8 +4,8 @@
 //
 // A CTA per SM walks its run of (256 rows x 128 keys) tiles:
 //  * warp 8 brings the tiles' keys and values, page by page, by TMA through a
-//    ring of 32 KB slots (keys, values, keys, ... in turn);
-//  * warps 10 and 11 gather a piece's queries while the piece before ends;
+//    ring of four tiles' sides (keys, values, keys, ... in turn);
+//  * warps 10 and 11 bring a piece's queries while the piece before ends;
 //  * warp 9 issues the products: S = Q K^T of both 128-row
 //    halves into tensor memory, later O += P V with P read from tensor
 //    memory, where it replaces S;
@@ -41,8 +41,9 @@ template <int D>
 struct WaShape {
     static constexpr int Q = WA_ROWS * D * 2;      // both halves' queries
     static constexpr int SLOT = WA_KEYS * D * 2;   // a tile's keys or values
-    static constexpr int SLOTS = 5 * 128 / D > 8 ? 8 : 5 * 128 / D;
-    static constexpr int SMEM = Q + SLOTS * SLOT + 1024;
+    static constexpr int SLOTS = 4 * 128 / D;
+    static constexpr int STAGE = 32 * 128;         // a rows' warp's results on their way out: 32 rows x 32 columns
+    static constexpr int SMEM = Q + SLOTS * SLOT + 8 * STAGE + 1024;
     // tensor memory columns: S of half q at 128 q (P, two bf16 a column, in its first 64), O at 256 + D q
     static constexpr uint32_t S0 = 0, O0 = 256;
 };
@@ -109,12 +110,13 @@ __device__ void wa_produce(const CUtensorMap &mk, const CUtensorMap &mv, const A
         ok = mbar_wait_now(&bar.full[i % S::SLOTS], (i / S::SLOTS) & 1, status);
 }
 
-// ---- the queries' warps: a half each of a piece's rows, gathered into the product's operand layout
+// ---- the queries' warps: a half each of a piece's rows, in the product's operand layout
 template <int D>
-__device__ void wa_queries(const AttnPlanDev &p, const AttnArgs &a, unsigned char *qsm, WaBars &bar, int half)
+__device__ void wa_queries(const CUtensorMap &mq, const AttnPlanDev &p, const AttnArgs &a, unsigned char *qsm,
+                           WaBars &bar, int half)
 {
     constexpr int CH = D / 8, STEP = 32 / CH;  // 16-byte chunks of a row; rows between a lane's
-    const int lane = threadIdx.x & 31, ch = lane % CH, first = half * WA_HALF + lane / CH;
+    const int lane = threadIdx.x & 31, ch = lane % CH;
     int32_t *status = p.hdr + AH_STATUS;
     const int G = p.hq / p.hkv;
     // the weights 2^(s c - m) want c > 0: a negative scale turns the queries' signs, a scale of 0 makes them 0
@@ -129,26 +131,36 @@ __device__ void wa_queries(const AttnPlanDev &p, const AttnArgs &a, unsigned cha
         if (n > 0 && !mbar_wait_now(&bar.q_free[half], (n - 1) & 1, status))
             return;
         ++n;
-#pragma unroll 8
-        for (int i = 0; i < WA_HALF; i += STEP) {
-            const int row = first + i, gr = g.row0 + row, t = (unsigned)gr / (unsigned)G;
-            unsigned char *d = dst + sw128_offset(row - half * WA_HALF, ch * 8, WA_HALF);
-            if (row < g.nrows)
-                cp_async16(d, a.q + t * a.q_stride + (long long)(w.h * G + gr - t * G) * D + ch * 8);
-            else
-                *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
-        }
-        cp_async_wait_all();
-        if (~q_and | q_xor)
-            for (int i = 0; i < WA_HALF; i += STEP) {
-                uint4 *d = reinterpret_cast<uint4 *>(dst + sw128_offset(lane / CH + i, ch * 8, WA_HALF));
-                const uint4 x = *d;
-                *d = make_uint4((x.x & q_and) ^ q_xor, (x.y & q_and) ^ q_xor, (x.z & q_and) ^ q_xor,
-                                (x.w & q_and) ^ q_xor);
+        if (a.q_map) {
+            // a half is a whole number of tokens and the map's boxes are halves (the rows after the segment's are
+            // other tokens', whose results go nowhere)
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar.q_full[half], WA_HALF * D * 2);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(dst + c * (WA_HALF * 128), &mq, c * 64, w.h * G, (g.row0 + half * WA_HALF) / G,
+                                &bar.q_full[half]);
             }
+            __syncwarp();
+            continue;
+        }
+#pragma unroll 4
+        for (int i = lane / CH; i < WA_HALF; i += STEP) {
+            const int row = half * WA_HALF + i, gr = g.row0 + row, t = (unsigned)gr / (unsigned)G;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (row < g.nrows)
+                x = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride +
+                                                     (long long)(w.h * G + gr - t * G) * D + ch * 8);
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(i, ch * 8, WA_HALF)) =
+                make_uint4((x.x & q_and) ^ q_xor, (x.y & q_and) ^ q_xor, (x.z & q_and) ^ q_xor, (x.w & q_and) ^ q_xor);
+        }
         fence_proxy_async_smem();
-        mbar_arrive(&bar.q_full[half]);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bar.q_full[half]);
     }
+    // the last load has landed before the CTA can exit
+    if (n > 0)
+        mbar_wait_now(&bar.q_full[half], (n - 1) & 1, status);
 }
 
 // ---- MMA warp
@@ -263,7 +275,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 // ---- softmax warps: thread = row
 template <int D>
 __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_bfloat16 *vcache, unsigned char *ring,
-                           WaBars &bar)
+                           unsigned char *stages, WaBars &bar)
 {
     typedef WaShape<D> S;
     const int tid = threadIdx.x, half = tid >> 7, r = tid & 127, lane = tid & 31;
@@ -272,6 +284,7 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
     const bool bad_pages = (*(volatile int32_t *)status & LORA_DEV_BAD_PAGE) != 0;
     const uint32_t quarter = (uint32_t)((r >> 5) * 32) << 16;  // this warp's tensor memory lanes
     const uint32_t ts = bar.taddr + quarter + S::S0 + half * 128, to = bar.taddr + quarter + S::O0 + half * D;
+    unsigned char *stage = stages + (tid >> 5) * S::STAGE;
     const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);  // (see wa_queries)
     int nt = 0;    // tiles of this half so far
     int it = 0;    // ring slots so far
@@ -391,19 +404,27 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
                     break;
                 }
                 unsigned char *v = ring + (vs % S::SLOTS) * S::SLOT;
-                bool odd = false;
-                for (int i = r; i < WA_KEYS * (D / 8); i += 128) {
+                auto chunk = [&](int i) {
                     const int key = i / (D / 8), ch = i % (D / 8);
-                    uint4 *at = reinterpret_cast<uint4 *>(v + (ch >> 3) * WA_KEYS * 128 + key * 128 +
-                                                          (((ch & 7) ^ (key & 7)) << 4));
-                    if (key0 + key >= g.nkeys) {
-                        *at = make_uint4(0, 0, 0, 0);
-                        continue;
+                    return reinterpret_cast<uint4 *>(v + (ch >> 3) * WA_KEYS * 128 + key * 128 +
+                                                     (((ch & 7) ^ (key & 7)) << 4));
+                };
+                // a bf16 whose exponent is all ones carries into its top bit
+                auto odd_word = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                uint32_t odd = 0;
+#pragma unroll 4
+                for (int i = r; i < WA_KEYS * (D / 8); i += 128) {
+                    if (key0 + i / (D / 8) >= g.nkeys) {
+                        *chunk(i) = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint4 x = *chunk(i);
+                        odd |= odd_word(x.x) | odd_word(x.y) | odd_word(x.z) | odd_word(x.w);
                     }
-                    uint4 x = *at;
-                    if (bf16_pair_not_finite(x.x) || bf16_pair_not_finite(x.y) || bf16_pair_not_finite(x.z) ||
-                        bf16_pair_not_finite(x.w)) {
-                        uint32_t e[4] = {x.x, x.y, x.z, x.w};
+                }
+                if (odd) {
+                    for (int i = r; i < WA_KEYS * (D / 8); i += 128) {
+                        uint4 *at = chunk(i);
+                        uint32_t e[4] = {at->x, at->y, at->z, at->w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (bf16_not_finite(e[j]))
@@ -412,11 +433,9 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
                                 e[j] &= 0x0000ffffu;
                         }
                         *at = make_uint4(e[0], e[1], e[2], e[3]);
-                        odd = true;
                     }
-                }
-                if (odd)
                     bar.poison = 1;
+                }
                 fence_proxy_async_smem();
             }
             tmem_wait_st();
@@ -465,11 +484,19 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
                     }
                 }
             }
-            if (valid) {
-                uint4 *x = reinterpret_cast<uint4 *>(p.part + out * D + i);
+            // through shared memory, so that eight lanes store a row's 128 bytes together
+            __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int rr = j * 4 + (lane >> 3);
+                if (row - lane + rr < g.nrows)
+                    *reinterpret_cast<uint4 *>(p.part + (out - lane + rr) * D + i + (lane & 7) * 4) =
+                        *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
             }
         }
         tc_fence_before();
@@ -478,8 +505,9 @@ __device__ void wa_softmax(const AttnPlanDev &p, const AttnArgs &a, const __nv_b
 
 template <int D>
 __global__ void __launch_bounds__(WA_THREADS, 1)
-    k_attn_wide(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnPlanDev p,
-                const AttnArgs a, const __nv_bfloat16 *vcache)
+    k_attn_wide(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                const __grid_constant__ CUtensorMap mq, const AttnPlanDev p, const AttnArgs a,
+                const __nv_bfloat16 *vcache)
 {
     typedef WaShape<D> S;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -493,7 +521,7 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
             mbar_init(&bar.empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) {
-            mbar_init(&bar.q_full[q], 32);
+            mbar_init(&bar.q_full[q], 1);
             mbar_init(&bar.q_free[q], 1);
             mbar_init(&bar.s_full[q], 1);
             mbar_init(&bar.p_full[q], 128);
@@ -511,13 +539,13 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
     pdl_launch_dependents();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WA_REGS_ROWS));
-        wa_softmax<D>(p, a, vcache, smem + S::Q, bar);
+        wa_softmax<D>(p, a, vcache, smem + S::Q, smem + S::Q + S::SLOTS * S::SLOT, bar);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WA_REGS_REST));
         if (warp == 8)
             wa_produce<D>(mk, mv, p, a.oob_row, smem + S::Q, bar);
         else if (warp >= 10)
-            wa_queries<D>(p, a, smem, bar, warp - 10);
+            wa_queries<D>(mq, p, a, smem, bar, warp - 10);
         else
             wa_mma<D>(p, smem_u32(smem), smem_u32(smem + S::Q), bar);
     }
@@ -545,8 +573,16 @@ cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cach
     CUtensorMap mk, mv;
     std::memcpy(&mk, cache.map_k[AC_WIDE], sizeof(mk));
     std::memcpy(&mv, cache.map_v[AC_WIDE], sizeof(mv));
+    // The queries of a half come by TMA where a half is a whole number of tokens and the scale needs no turn of
+    // their signs; the gather loop that takes them otherwise costs up to 18,000 cycles a piece.
+    CUtensorMap mq = mk;
+    AttnArgs aw = a;
+    const int G = p.hq / p.hkv;
+    aw.q_map = a.scale_log2 > 0.f && WA_HALF % G == 0 &&
+               encode_q_heads(&mq, a.q, p.d, p.hq, a.TQ, a.q_stride, G, WA_HALF / G) == cudaSuccess;
     const __nv_bfloat16 *v = cache.v;
-    return launch_pdl(k_attn_wide<D>, dim3(p.workers[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, p, a, v);
+    return launch_pdl(k_attn_wide<D>, dim3(p.workers[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, mq, p,
+                      aw, v);
 }
 
 }  // namespace

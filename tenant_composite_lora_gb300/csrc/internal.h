@@ -207,6 +207,10 @@ struct MmaMaps {
 cudaError_t mma_encode_maps(const PoolDev &pool, MmaMaps &maps);
 // A tensor map over a cache side's rows [rows][d]: boxes of box_rows rows x 64 columns, 128-byte swizzle.
 cudaError_t encode_kv_rows(unsigned char *map, const void *base, int d, long long rows, int box_rows);
+// A tensor map (CUtensorMap at out) over queries [tokens][heads][d], tokens stride elements apart: boxes of
+// box_tokens tokens x box_heads heads x 64 columns, 128-byte swizzle.
+cudaError_t encode_q_heads(void *out, const void *q, int d, int heads, int tokens, long long stride, int box_heads,
+                           int box_tokens);
 bool mma_supported(int d_in, int d_out, int r_max);
 cudaError_t launch_mma(const __nv_bfloat16 *x, __nv_bfloat16 *y, const PoolDev &pool, const MmaMaps &maps,
                        const int32_t *ranks, const MapDev &m, int T, int P, cudaStream_t st);

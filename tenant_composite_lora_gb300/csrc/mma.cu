@@ -1047,6 +1047,22 @@ cudaError_t encode_kv_rows(unsigned char *map, const void *base, int d, long lon
     return encode_rows(map, base, d, rows, box_rows);
 }
 
+cudaError_t encode_q_heads(void *out, const void *q, int d, int heads, int tokens, long long stride, int box_heads,
+                           int box_tokens)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(static_cast<CUtensorMap *>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q),
+                          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 bool mma_supported(int d_in, int d_out, int r_max)
 {
     return d_in % 64 == 0 && d_out % 64 == 0 && r_max >= 1 && r_max <= LORA_MAX_RANK;
