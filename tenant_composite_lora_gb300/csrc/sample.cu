@@ -7,14 +7,22 @@
 // describes it.  Masses are 64-bit fixed point, e * 2^40 (V <= 2^20 terms of
 // at most 2^40), so their sums do not depend on the order.
 //
-// A cluster of CTAs holds a row in registers (one read of the logits): the
-// maximum, then a bound below which no kept token can lie -- the top-k's
-// from the threads' own maxima, min-p's from its definition, top-p's from
-// the mass above a few trial bounds -- then the few candidates above it,
-// gathered by one CTA, which cuts and picks.  Rows whose
-// candidates are too many for that (nearly flat ones) find the cut by
-// bisection over the registers, counts and masses joined over the cluster.
-// Bound by the logits' bytes and the latency of the cluster's barriers.
+//  1. The maximum, and with a top-k a bound that at least k tokens reach,
+//     from the threads' own maxima.
+//  2. A bound below which no kept token lies: that one, min-p's from its
+//     definition, top-p's from the mass above a few trial bounds.
+//  3. The few candidates above it go to one CTA, which cuts and picks.
+//  4. Rows with too many of them (nearly flat ones): the cut is searched
+//     for, three thresholds a pass, until so few tokens are left around it
+//     that one CTA can take those; then the kept masses in index order.
+//
+// Two forms of one kernel.  With few rows a cluster of CTAs holds a row in
+// registers (one read of the logits); with many, or with rows too long for
+// that, a CTA a row reads it again from the L2 in each pass, so that all
+// rows are under way at once.  Bound by the logits' bytes and by the latency
+// of the steps, some ten barriers a row.
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -22,7 +30,12 @@ namespace tcl {
 
 namespace {
 
-constexpr int SA_THREADS = 1024;
+constexpr int SC_THREADS = 512, SC_WARPS = SC_THREADS / 32;
+constexpr int SC_LIST = 2048;   // candidates that one CTA takes
+constexpr int SC_SLOTS = 4096;  // places for them, an equal share for each CTA of the cluster
+constexpr int SC_FEW = 256;     // of these, those that are compared each with each
+constexpr int SC_MAX_CLUSTER = 16;
+static_assert(SC_MAX_CLUSTER <= SC_WARPS, "a warp moves a CTA's candidates");
 
 struct SampleArgs {
     const void *logits;
@@ -36,19 +49,27 @@ struct SampleArgs {
 
 typedef unsigned long long u64;
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T *row, int i);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float *row, int i)
+// ---------------------------------------------------------------- numbers
+
+// Unsigned integers in the order of the floats.
+__device__ __forceinline__ uint32_t order_key(float l)
 {
-    const float l = row[i] + 0.f;  // -0 counts as 0
-    return isnan(l) ? -INFINITY : l;
+    const uint32_t b = __float_as_uint(l);
+    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
-template <>
-__device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16 *row, int i)
+__device__ __forceinline__ float key_logit(uint32_t key)
 {
-    const float l = __bfloat162float(row[i]) + 0.f;
-    return isnan(l) ? -INFINITY : l;
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+constexpr uint32_t KEY_LOWEST = 0x007fffffu;  // of -inf
+
+// e * 2^40 rounded down, for 0 <= e < 2^15: in two exact parts of 32 bits.
+__device__ __forceinline__ u64 fixed_mass(float e)
+{
+    const float x = e * 65536.f;
+    const uint32_t hi = __float2uint_rz(x);
+    const uint32_t lo = __float2uint_rz((x - __uint2float_rz(hi)) * 16777216.f);
+    return ((u64)hi << 24) + lo;
 }
 
 // x in [0, 1) as a 64-bit fraction (exact from 2^-40 on), in two exact parts.
@@ -79,287 +100,34 @@ __device__ __forceinline__ u64 goal_mass(float u, u64 z)
 
 __device__ __forceinline__ float share(float e, u64 z) { return e / (__ull2float_rn(z) * 0x1p-40f); }
 
-// Unsigned integers in the order of the floats.
-__device__ __forceinline__ uint32_t order_key(float l)
-{
-    const uint32_t b = __float_as_uint(l);
-    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-}
-
-struct RowScale {
-    float m, inv;
-    __device__ __forceinline__ float e(float l) const
-    {
-        return l == -INFINITY ? 0.f : l == m ? 1.f : expf((l - m) * inv);
-    }
-    __device__ __forceinline__ u64 mass(float l) const { return __float2ull_rn(e(l) * 1099511627776.f); }
-};
-
-template <typename V>
-__device__ V block_sum(V v, V *sh)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    V r = 0;
-    for (int w = 0; w < SA_THREADS / 32; ++w)
-        r += sh[w];
-    return r;
-}
-
-// Exclusive sum over the threads before this one.
-template <typename V>
-__device__ V block_before(V v, V *sh)
-{
-    const int lane = threadIdx.x & 31;
-    V inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o)
-            inc += x;
-    }
-    __syncthreads();
-    if (lane == 31)
-        sh[threadIdx.x >> 5] = inc;
-    __syncthreads();
-    V r = inc - v;
-    for (int w = 0; w < (int)(threadIdx.x >> 5); ++w)
-        r += sh[w];
-    return r;
-}
-
-// A CTA per row, for rows too long for a cluster's registers.
-template <typename T>
-__global__ void __launch_bounds__(SA_THREADS) k_sample_simple(const SampleArgs a)
-{
-    __shared__ u64 sh[32], hist[256];
-    __shared__ float shf[32];
-    __shared__ u64 s_run;
-    __shared__ uint32_t s_key;
-    __shared__ int s_idx;
-    const int r = blockIdx.x, tid = threadIdx.x, V = a.V;
-    const T *row = static_cast<const T *>(a.logits) + r * a.stride;
-
-    float m = -INFINITY;
-    for (int i = tid; i < V; i += SA_THREADS)
-        m = fmaxf(m, load_logit(row, i));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0)
-        shf[tid >> 5] = m;
-    __syncthreads();
-    for (int w = 0; w < SA_THREADS / 32; ++w)
-        m = fmaxf(m, shf[w]);
-    if (m == -INFINITY) {
-        if (tid == 0) {
-            a.tokens[r] = -1;
-            if (a.probs)
-                a.probs[r] = 0.f;
-        }
-        return;
-    }
-    const float tau = a.tau ? a.tau[r] : 1.f;
-    const bool greedy = !(tau > 0.f);
-    const RowScale sc{m, greedy ? 1.f : 1.f / tau};
-    const int k = greedy ? 1 : a.top_k ? a.top_k[r] : 0;
-    const float p = greedy || !a.top_p ? 1.f : a.top_p[r];
-    const float mp = greedy || !a.min_p || !(a.min_p[r] > 0.f) ? 0.f : fminf(a.min_p[r], 1.f);
-
-    // first k: the cut's key and how many of its ties stay
-    uint32_t cut = 0;
-    u64 ties = ~0ull;  // all
-    if (k > 0 && k < V) {
-        u64 need = (u64)k;
-        uint32_t pre = 0;
-        for (int sft = 24; sft >= 0; sft -= 8) {
-            if (tid < 256)
-                hist[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < V; i += SA_THREADS) {
-                const uint32_t key = order_key(load_logit(row, i));
-                if (sft == 24 || (key >> (sft + 8)) == (pre >> (sft + 8)))
-                    atomicAdd(&hist[(key >> sft) & 255], 1ull);
-            }
-            __syncthreads();
-            if (tid == 0) {
-                int b = 255;
-                while (hist[b] < need)
-                    need -= hist[b--];
-                s_key = pre | ((uint32_t)b << sft);
-                s_run = need;
-            }
-            __syncthreads();
-            pre = s_key;
-            need = s_run;
-        }
-        cut = pre;
-        ties = need;
-    }
-    // mass of those, then the shortest prefix of them that reaches top_p of it
-    u64 above = 0, equal = 0;
-    float cut_l = -INFINITY;
-    if (cut) {
-        const uint32_t b = cut ^ ((cut >> 31) ? 0x80000000u : 0xffffffffu);
-        cut_l = __uint_as_float(b);
-    }
-    for (int i = tid; i < V; i += SA_THREADS) {
-        const float l = load_logit(row, i);
-        const uint32_t key = order_key(l);
-        if (key > cut)
-            above += sc.mass(l);
-        equal += key == cut;
-    }
-    above = block_sum(above, sh);
-    equal = block_sum(equal, sh);
-    if (ties > equal)
-        ties = equal;
-    const u64 zk = above + ties * sc.mass(cut_l);
-    if (p < 1.f) {
-        const u64 need_of_zk = needed_mass(p, zk);
-        u64 need = need_of_zk;
-        if (above >= need) {  // the cut moves up
-            uint32_t pre = 0;
-            const uint32_t kcut = cut;
-            for (int sft = 24; sft >= 0; sft -= 8) {
-                if (tid < 256)
-                    hist[tid] = 0;
-                __syncthreads();
-                for (int i = tid; i < V; i += SA_THREADS) {
-                    const float l = load_logit(row, i);
-                    const uint32_t key = order_key(l);
-                    if (key > kcut && (sft == 24 || (key >> (sft + 8)) == (pre >> (sft + 8))))
-                        atomicAdd(&hist[(key >> sft) & 255], sc.mass(l));
-                }
-                __syncthreads();
-                if (tid == 0) {
-                    int b = 255;
-                    while (hist[b] < need)
-                        need -= hist[b--];
-                    s_key = pre | ((uint32_t)b << sft);
-                    s_run = need;
-                }
-                __syncthreads();
-                pre = s_key;
-                need = s_run;
-            }
-            cut = pre;
-            const u64 w = sc.mass(__uint_as_float(cut ^ ((cut >> 31) ? 0x80000000u : 0xffffffffu)));
-            ties = (need + w - 1) / w;
-        } else {
-            const u64 w = sc.mass(cut_l);
-            if (w > 0) {
-                const u64 t = (need - above + w - 1) / w;
-                ties = t < ties ? t : ties;
-            }
-        }
-    }
-    // ties stay by index: the last one's index; then the masses in index order
-    const int per = (V + SA_THREADS - 1) / SA_THREADS, i0 = min(V, tid * per), i1 = min(V, i0 + per);
-    u64 mine = 0;
-    for (int i = i0; i < i1; ++i)
-        mine += order_key(load_logit(row, i)) == cut;
-    const u64 before = block_before(mine, sh);
-    if (tid == 0)
-        s_idx = ties == 0 ? -1 : V;
-    __syncthreads();
-    if (ties > 0 && before < ties && ties <= before + mine) {
-        u64 n = before;
-        for (int i = i0; i < i1; ++i)
-            if (order_key(load_logit(row, i)) == cut && ++n == ties) {
-                s_idx = i;
-                break;
-            }
-    }
-    __syncthreads();
-    const int last_tie = s_idx;
-    auto kept_mass = [&](int i) -> u64 {
-        const float l = load_logit(row, i);
-        const uint32_t key = order_key(l);
-        if (key < cut || (key == cut && i > last_tie))
-            return 0;
-        const float e = sc.e(l);
-        return e >= mp ? __float2ull_rn(e * 1099511627776.f) : 0;
-    };
-    u64 seg = 0;
-    for (int i = i0; i < i1; ++i)
-        seg += kept_mass(i);
-    const u64 z = block_sum(seg, sh);
-    const u64 run0 = block_before(seg, sh);
-    const float u = a.u[r];
-    const u64 goal = goal_mass(u, z);
-    if (run0 <= goal && goal < run0 + seg) {
-        u64 c = run0;
-        for (int i = i0; i < i1; ++i) {
-            c += kept_mass(i);
-            if (c > goal) {
-                a.tokens[r] = i;
-                if (a.probs)
-                    a.probs[r] = share(sc.e(load_logit(row, i)), z);
-                break;
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------- a cluster per row
-
-constexpr int SC_THREADS = 512, SC_WARPS = SC_THREADS / 32;
-constexpr int SC_LIST = 2048;   // candidates that one CTA takes
-constexpr int SC_SLOTS = 4096;  // places for them, an equal share for each CTA of the cluster
-constexpr int SC_TRIALS = 3;   // trial bounds of the top-p: e >= 2^-8, 2^-14, 2^-20
-constexpr int SC_MAX_CLUSTER = 16;
-static_assert(SC_MAX_CLUSTER <= SC_WARPS, "a warp moves a CTA's candidates");
-
-__device__ __forceinline__ float key_logit(uint32_t key)
-{
-    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
-// e * 2^40 rounded down, for 0 <= e < 2^15: in two exact parts of 32 bits.
-__device__ __forceinline__ u64 fixed_mass(float e)
-{
-    const float x = e * 65536.f;
-    const uint32_t hi = __float2uint_rz(x);
-    const uint32_t lo = __float2uint_rz((x - __uint2float_rz(hi)) * 16777216.f);
-    return ((u64)hi << 24) + lo;
-}
-
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// ---------------------------------------------------------------- sums over warp, CTA, cluster
 
 template <typename V>
 __device__ __forceinline__ void st_cluster(V *local, uint32_t rank, V x)
 {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-    if constexpr (sizeof(V) == 8)
-        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
-    else
-        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
 }
 
 struct SampleShared {
-    // rank 0: the candidates (order key inverted, index), SC_SLOTS / C places for each CTA's; then all in a row
+    // rank 0: the candidates (order key, index), SC_SLOTS / C places for each CTA's; then all in a row, by index
     alignas(16) u64 slots[SC_SLOTS];
     alignas(16) u64 list[SC_LIST];
-    alignas(16) u64 mass[SC_THREADS];  // theirs, where they are few
-    u64 warp64[SC_WARPS];
+    alignas(16) u64 mass[SC_FEW];  // theirs, where they are few
     uint32_t warp32[SC_WARPS];
     uint32_t packed[2][SC_WARPS];
-    // words exchanged over the cluster, two sets used in turn
+    // words exchanged over the cluster and the CTA, two sets used in turn
     u64 x64[2][8][SC_MAX_CLUSTER];
     u64 part[2][8][SC_WARPS];
-    uint32_t count;
+    u64 cut;
 };
 // (dynamic shared memory, whose address space functions that are not inlined know too)
 __device__ __forceinline__ SampleShared &sample_shared()
@@ -367,6 +135,21 @@ __device__ __forceinline__ SampleShared &sample_shared()
     extern __shared__ __align__(16) unsigned char sample_smem[];
     return *reinterpret_cast<SampleShared *>(sample_smem);
 }
+
+// A thread's place, and the count of exchanges so far: sets of words are
+// used in turn, so that one barrier an exchange is enough.
+struct Place {
+    int C;
+    uint32_t rank;
+    int lane, warp, turn;
+    __device__ __forceinline__ void barrier() const
+    {
+        if (C > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    }
+};
 
 __device__ __forceinline__ u64 warp_sum64(u64 v)
 {
@@ -376,335 +159,366 @@ __device__ __forceinline__ u64 warp_sum64(u64 v)
     return v;
 }
 
-// Sums of N words over the cluster's threads (WARP: its warps, whose lanes
-// hold the same); every thread gets them.
-// `turn` counts the calls: the words' two sets are used alternately, so that
-// one barrier a call is enough.
-template <bool WARP, int N>
-__device__ __forceinline__ void cluster_sums(u64 (&v)[N], SampleShared &sh, int &turn, int C, uint32_t rank)
+// Sums of N words over the cluster's warps, whose lanes hold the same; every
+// thread gets them.
+template <int N>
+__device__ __forceinline__ void cluster_sums(u64 (&v)[N], Place &at)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int set = turn++ & 1;
-    auto &part = sh.part;
+    SampleShared &sh = sample_shared();
+    const int set = at.turn++ & 1;
+    if (at.lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const u64 w = WARP ? v[i] : warp_sum64(v[i]);
-        if (lane == 0)
-            part[set][i][warp] = w;
-    }
+        for (int i = 0; i < N; ++i)
+            sh.part[set][i][at.warp] = v[i];
     __syncthreads();
-    if (warp < N) {
-        u64 w = lane < SC_WARPS ? part[set][warp][lane] : 0;
-        w = warp_sum64(w);
-        if (lane < C)
-            st_cluster(&sh.x64[set][warp][rank], (uint32_t)lane, w);
+    if (at.C == 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = sh.part[set][i][at.lane % SC_WARPS];
+#pragma unroll
+        for (int o = SC_WARPS / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        return;
     }
-    if (C > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    if (at.warp < N) {
+        u64 w = at.lane < SC_WARPS ? sh.part[set][at.warp][at.lane] : 0;
+        w = warp_sum64(w);
+        if (at.lane < at.C)
+            st_cluster(&sh.x64[set][at.warp][at.rank], (uint32_t)at.lane, w);
+    }
+    cluster_sync();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         u64 t = 0;
-        for (int r = 0; r < C; ++r)
+        for (int r = 0; r < at.C; ++r)
             t += sh.x64[set][i][r];
         v[i] = t;
     }
 }
 
-// The sum over the threads and CTAs before this one, and over all.
-__device__ __forceinline__ u64 cluster_before(u64 v, u64 &all, SampleShared &sh, int &turn, int C, uint32_t rank)
+// The sum over the cluster's warps before this one, and over all.
+__device__ __forceinline__ u64 cluster_before(u64 v, u64 &all, Place &at)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int set = turn++ & 1;
-    u64 inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o)
-            inc += x;
-    }
+    SampleShared &sh = sample_shared();
+    const int set = at.turn++ & 1;
+    if (at.lane == 0)
+        sh.part[set][0][at.warp] = v;
     __syncthreads();
-    if (lane == 31)
-        sh.warp64[warp] = inc;
-    __syncthreads();
-    u64 before = inc - v, mine = 0;
+    u64 before = 0, mine = 0;
     for (int w = 0; w < SC_WARPS; ++w) {
-        if (w < warp)
-            before += sh.warp64[w];
-        mine += sh.warp64[w];
+        const u64 y = sh.part[set][0][w];
+        before += w < at.warp ? y : 0;
+        mine += y;
     }
-    if (threadIdx.x < C)
-        st_cluster(&sh.x64[set][0][rank], (uint32_t)threadIdx.x, mine);
-    if (C > 1)
+    all = mine;
+    if (at.C > 1) {
+        if (threadIdx.x < at.C)
+            st_cluster(&sh.x64[set][0][at.rank], threadIdx.x, mine);
         cluster_sync();
-    else
-        __syncthreads();
-    all = 0;
-    for (int r = 0; r < C; ++r) {
-        if (r < (int)rank)
-            before += sh.x64[set][0][r];
-        all += sh.x64[set][0][r];
+        all = 0;
+        for (int r = 0; r < at.C; ++r) {
+            const u64 y = sh.x64[set][0][r];
+            before += r < (int)at.rank ? y : 0;
+            all += y;
+        }
     }
     return before;
 }
 
-// Sum over the block of a value, to all threads.
-__device__ __forceinline__ u64 block_sum64(u64 v, SampleShared &sh)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = warp_sum64(v);
-    __syncthreads();
-    if (lane == 0)
-        sh.warp64[warp] = v;
-    __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int w = 0; w < SC_WARPS; ++w)
-        t += sh.warp64[w];
-    return t;
-}
-
-// Rank 0 of a row's cluster: sh.list holds its n <= SC_THREADS candidates.
-// Each candidate's place in the order and the masses before it come from a
-// comparison with every other one (S threads share a candidate's), which for
-// so few is shorter than a sort's or a bisection's barriers.
-template <int S>
-__device__ __noinline__ void pick_by_counting(const SampleArgs &a, int r, int n, int k, bool has_p, float p, float mp,
-                                              float u, float m, float inv, u64 z_all)
+// Within rank 0: sums of N values over the threads, and the sum over the
+// threads before this one.
+template <int N>
+__device__ __forceinline__ void block_sums(u64 (&v)[N], int &turn)
 {
     SampleShared &sh = sample_shared();
-    const int i = threadIdx.x / S, part = threadIdx.x % S;
-    const bool live = i < n;
-    u64 *mass = sh.mass;
-    const u64 x = live ? sh.list[i] : ~0ull;
-    const float e = live ? expf((key_logit(~(uint32_t)(x >> 32)) - m) * inv) : 0.f;
-    const u64 w = fixed_mass(e);
-    // padded to whole steps (at most SC_THREADS / S places) with places behind all others, of no mass
-    const int np = (n + 4 * S - 1) / (4 * S) * (4 * S);
-    if (part == 0 && i < np) {
-        mass[i] = w;
-        if (!live)
-            sh.list[i] = ~0ull;
-    }
-    __syncthreads();
-    auto shared_sum = [&](u64 v) {
-#pragma unroll
-        for (int o = S / 2; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    };
-    u64 before = 0;
-    uint32_t rank = 0;
-    if (__any_sync(0xffffffffu, live)) {
-        for (int j = 2 * part; j < np; j += 4 * S) {
-            const ulonglong2 l0 = *reinterpret_cast<const ulonglong2 *>(&sh.list[j]);
-            const ulonglong2 l1 = *reinterpret_cast<const ulonglong2 *>(&sh.list[j + 2 * S]);
-            const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(&mass[j]);
-            const ulonglong2 m1 = *reinterpret_cast<const ulonglong2 *>(&mass[j + 2 * S]);
-            rank += (uint32_t)(l0.x < x) + (uint32_t)(l0.y < x) + (uint32_t)(l1.x < x) + (uint32_t)(l1.y < x);
-            before += (l0.x < x ? m0.x : 0) + (l0.y < x ? m0.y : 0) + (l1.x < x ? m1.x : 0) + (l1.y < x ? m1.y : 0);
-        }
-        before = shared_sum(before);
-#pragma unroll
-        for (int o = S / 2; o > 0; o >>= 1)
-            rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    }
-    const bool top = live && (k <= 0 || rank < (uint32_t)k);
-    u64 need = ~0ull;
-    if (has_p) {
-        const u64 zk = k > 0 ? block_sum64(top && part == 0 ? w : 0, sh) : z_all;
-        need = needed_mass(p, zk);
-    }
-    const bool keep = top && (rank == 0 || (before < need && e >= mp));
-    const u64 z = block_sum64(keep && part == 0 ? w : 0, sh);  // (its barriers: all have read mass[])
-    if (live && part == 0)
-        mass[i] = keep ? w : 0;
-    __syncthreads();
-    const u64 goal = goal_mass(u, z);
-    if (!__any_sync(0xffffffffu, keep))
-        return;
-    const uint32_t idx = (uint32_t)x;
-    before = 0;
-    for (int j = 2 * part; j < np; j += 4 * S) {
-        const ulonglong2 l0 = *reinterpret_cast<const ulonglong2 *>(&sh.list[j]);
-        const ulonglong2 l1 = *reinterpret_cast<const ulonglong2 *>(&sh.list[j + 2 * S]);
-        const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(&mass[j]);
-        const ulonglong2 m1 = *reinterpret_cast<const ulonglong2 *>(&mass[j + 2 * S]);
-        before += ((uint32_t)l0.x < idx ? m0.x : 0) + ((uint32_t)l0.y < idx ? m0.y : 0) +
-                  ((uint32_t)l1.x < idx ? m1.x : 0) + ((uint32_t)l1.y < idx ? m1.y : 0);
-    }
-    before = shared_sum(before);
-    if (keep && part == 0 && before <= goal && goal < before + w) {
-        a.tokens[r] = (int)idx;
-        if (a.probs)
-            a.probs[r] = share(e, z);
-    }
-}
-
-// Sums of N values over the block, to all threads; `turn` alternates the buffers.
-template <int N>
-__device__ __forceinline__ void block_sums(u64 (&v)[N], SampleShared &sh, int &turn)
-{
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = turn++ & 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[i] = warp_sum64(v[i]);
         if (lane == 0)
-            sh.x64[set][i][warp] = v[i];
+            sh.part[set][i][warp] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        u64 t = 0;
+    for (int i = 0; i < N; ++i)
+        v[i] = sh.part[set][i][lane % SC_WARPS];
 #pragma unroll
-        for (int w = 0; w < SC_WARPS; ++w)
-            t += sh.x64[set][i][w];
-        v[i] = t;
+    for (int o = SC_WARPS / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+__device__ __forceinline__ u64 block_before(u64 v, u64 &all, int &turn)
+{
+    SampleShared &sh = sample_shared();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = turn++ & 1;
+    u64 inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o)
+            inc += y;
+    }
+    if (lane == 31)
+        sh.part[set][0][warp] = inc;
+    __syncthreads();
+    u64 t = lane < SC_WARPS ? sh.part[set][0][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < SC_WARPS; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o)
+            t += y;
+    }
+    all = __shfl_sync(0xffffffffu, t, SC_WARPS - 1);
+    const u64 w = __shfl_sync(0xffffffffu, t, warp > 0 ? warp - 1 : 0);
+    return inc - v + (warp > 0 ? w : 0);
+}
+
+// ---------------------------------------------------------------- one CTA's list
+
+struct PickArgs {
+    int r, n, k;  // row, candidates, top-k (0: off)
+    bool has_p;
+    float p, mp, u, m, inv;
+    u64 z_all;
+    int turn;
+};
+
+// Rank 0: sh.list holds the row's n candidates (order key, then index) by
+// index.
+//
+// At most SC_FEW: each one's place in the order and the mass before it come
+// from a comparison with every other one (S threads share one), without a
+// step that waits for the one before.
+template <int S>
+__device__ __noinline__ void pick_of_few(const SampleArgs &a, const PickArgs g)
+{
+    SampleShared &sh = sample_shared();
+    int turn = g.turn;
+    const int i = threadIdx.x / S, part = threadIdx.x % S, n = g.n;
+    const bool live = i < n;
+    const u64 x = live ? sh.list[i] : 0;
+    // (a larger key, or the same and a lower index, comes first: so does a larger one of these)
+    const u64 place = (x & 0xffffffff00000000ull) | (uint32_t)~(uint32_t)x;
+    const float e = live ? expf((key_logit((uint32_t)(x >> 32)) - g.m) * g.inv) : 0.f;
+    const u64 w = fixed_mass(e);
+    // padded to whole steps (at most SC_THREADS / S places) with places behind all others, of no mass
+    const int np = (n + 4 * S - 1) / (4 * S) * (4 * S);
+    if (part == 0 && i < np) {
+        sh.mass[i] = w;
+        sh.slots[i] = live ? place : 0;
+    }
+    __syncthreads();
+    u64 before = 0;
+    uint32_t rank = 0;
+    if (__any_sync(0xffffffffu, live)) {
+        if (g.has_p)
+            for (int j = 2 * part; j < np; j += 4 * S) {
+                const ulonglong2 l0 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j]);
+                const ulonglong2 l1 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j + 2 * S]);
+                const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(&sh.mass[j]);
+                const ulonglong2 m1 = *reinterpret_cast<const ulonglong2 *>(&sh.mass[j + 2 * S]);
+                before += (l0.x > place ? m0.x : 0) + (l0.y > place ? m0.y : 0) + (l1.x > place ? m1.x : 0) +
+                          (l1.y > place ? m1.y : 0);
+            }
+        // (the first has nothing before it; without a top-k that is all the rank is for)
+        if (g.k > 0 || !g.has_p)
+            for (int j = 2 * part; j < np; j += 4 * S) {
+                const ulonglong2 l0 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j]);
+                const ulonglong2 l1 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j + 2 * S]);
+                rank += (uint32_t)(l0.x > place) + (uint32_t)(l0.y > place) + (uint32_t)(l1.x > place) +
+                        (uint32_t)(l1.y > place);
+            }
+        else
+            rank = before > 0;
+#pragma unroll
+        for (int o = S / 2; o > 0; o >>= 1) {
+            rank += __shfl_xor_sync(0xffffffffu, rank, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+    }
+    const bool top = live && (g.k <= 0 || rank < (uint32_t)g.k);
+    u64 need = ~0ull;
+    if (g.has_p) {
+        u64 zk[1] = {top && part == 0 ? w : 0};
+        if (g.k > 0)
+            block_sums(zk, turn);
+        need = needed_mass(g.p, g.k > 0 ? zk[0] : g.z_all);
+    }
+    const bool keep = top && part == 0 && (rank == 0 || (before < need && e >= g.mp));
+    u64 z;
+    const u64 run = block_before(keep ? w : 0, z, turn), goal = goal_mass(g.u, z);
+    if (keep && run <= goal && goal < run + w) {
+        a.tokens[g.r] = (int)(uint32_t)x;
+        if (a.probs)
+            a.probs[g.r] = share(e, z);
     }
 }
 
-// The same for up to SC_LIST candidates, a few in each thread's registers:
-// the cut's key, the last kept tie's index and the token's index by
-// bisection, two bits a step.
-__device__ __noinline__ void pick_by_bisection(const SampleArgs &a, int r, int n, int k, bool has_p, float p, float mp,
-                                               float u, float m, float inv, u64 z_all)
-{
-    SampleShared &sh = sample_shared();
-    constexpr int PER = SC_LIST / SC_THREADS;
-    const int tid = threadIdx.x;
+// The list in registers, consecutive entries in a thread.
+struct ListRegs {
+    static constexpr int PER = SC_LIST / SC_THREADS;
     uint32_t key[PER], idx[PER];
     float e[PER];
     u64 w[PER];
-    uint32_t least = 0xffffffffu;
+    int top, bot;     // the keys differ in bits bot .. top - 1 only
+    uint32_t common;  // the bits that they share (0 in those in which they differ)
+
+    __device__ __forceinline__ void load(int n, float m, float inv)
+    {
+        SampleShared &sh = sample_shared();
+        const int tid = threadIdx.x;
+        const uint32_t some = (uint32_t)(sh.list[0] >> 32);
+        uint32_t differ = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int at = tid + i * SC_THREADS;
-        const u64 x = at < n ? sh.list[at] : ~0ull;
-        key[i] = ~(uint32_t)(x >> 32);  // (0, below every token's, where there is none)
-        idx[i] = (uint32_t)x;
-        e[i] = at < n ? expf((key_logit(key[i]) - m) * inv) : 0.f;
-        w[i] = fixed_mass(e[i]);
-        if (at < n)
-            least = min(least, key[i]);
+        for (int i = 0; i < PER; ++i) {
+            const int at = tid * PER + i;
+            const u64 x = at < n ? sh.list[at] : 0;
+            key[i] = (uint32_t)(x >> 32);  // (0, below every token's, where there is none)
+            idx[i] = (uint32_t)x;
+            e[i] = at < n ? expf((key_logit(key[i]) - m) * inv) : 0.f;
+            w[i] = fixed_mass(e[i]);
+            if (at < n)
+                differ |= key[i] ^ some;
+        }
+        differ = __reduce_or_sync(0xffffffffu, differ);
+        if ((tid & 31) == 0)
+            sh.warp32[tid >> 5] = differ;
+        __syncthreads();
+        differ = __reduce_or_sync(0xffffffffu, sh.warp32[tid % SC_WARPS]);
+        top = (33 - __clz(differ)) / 2 * 2;
+        bot = differ ? (__ffs(differ) - 1) / 2 * 2 : 0;
+        common = (top >= 32 ? 0u : some >> top << top) | (some & ((1u << bot) - 1));
     }
-    __syncthreads();
-    int turn = 0;
-    least = __reduce_min_sync(0xffffffffu, least);
-    if ((tid & 31) == 0)
-        sh.warp32[tid >> 5] = least;
-    __syncthreads();
-    for (int v = 0; v < SC_WARPS; ++v)
-        least = min(least, sh.warp32[v]);
-    // the keys differ in their bits below `top` only
-    const uint32_t most = order_key(m);
-    const int top = least == most ? 0 : (33 - __clz(least ^ most)) / 2 * 2;
-    const uint32_t common = top >= 32 ? 0u : most >> top << top;
-    uint32_t cut = 0;
-    u64 ties = ~0ull, over = 0;  // ties of the cut that are kept; mass above it
-    if (k > 0 && k < n) {
+
+    // The largest key that `need` of the mass (or of the tokens) above
+    // `floor` reaches, and what lies above it.
+    __device__ __forceinline__ uint32_t search(bool by_mass, u64 need, uint32_t floor, u64 &over, int &turn) const
+    {
         uint32_t lo = common;
-        u64 more = 0;  // tokens above the cut
-        for (int bit = top - 2; bit >= 0; bit -= 2) {
-            const uint32_t one = 1u << bit;
-            u64 c[2] = {};
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                c[0] += (u64)(key[i] >= lo + one) | (u64)(key[i] >= lo + 2 * one) << 32;
-                c[1] += key[i] >= lo + 3 * one;
-            }
-            block_sums(c, sh, turn);
-            const u64 q[3] = {c[0] & 0xffffffffu, c[0] >> 32, c[1]};
-            const int up = q[2] >= (u64)k ? 3 : q[1] >= (u64)k ? 2 : q[0] >= (u64)k ? 1 : 0;
-            lo += up * one;
-            if (up < 3)
-                more = q[up];
-        }
-        cut = lo;
-        ties = (u64)k - more;
-    }
-    if (has_p) {
-        u64 c[1] = {};
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            c[0] += key[i] > cut ? w[i] : 0;
-        block_sums(c, sh, turn);
-        const u64 w_cut = cut ? fixed_mass(expf((key_logit(cut) - m) * inv)) : 0;
-        const u64 zk = k > 0 ? c[0] + (cut ? ties * w_cut : 0) : z_all;
-        const u64 need = needed_mass(p, zk);
-        if (c[0] >= need) {
-            uint32_t lo = common;
-            for (int bit = top - 2; bit >= 0; bit -= 2) {
-                const uint32_t one = 1u << bit;
-                u64 f[3] = {};
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const u64 x = key[i] > cut ? w[i] : 0;
-                    f[0] += key[i] >= lo + one ? x : 0;
-                    f[1] += key[i] >= lo + 2 * one ? x : 0;
-                    f[2] += key[i] >= lo + 3 * one ? x : 0;
-                }
-                block_sums(f, sh, turn);
-                const int up = f[2] >= need ? 3 : f[1] >= need ? 2 : f[0] >= need ? 1 : 0;
-                lo += up * one;
-                if (up < 3)
-                    over = f[up];
-            }
-            cut = lo;
-            const u64 x = fixed_mass(expf((key_logit(cut) - m) * inv));
-            ties = x > 0 ? (need - over + x - 1) / x : 1;
-        } else if (cut && w_cut > 0) {
-            ties = min(ties, (need - c[0] + w_cut - 1) / w_cut);
-        }
-    }
-    // the least index at which a running sum over the tokens, by index, exceeds `goal`
-    auto at_index = [&](const u64 (&x)[PER], u64 goal) {
-        uint32_t lo = 0;
-        for (int bit = 20; bit >= 0; bit -= 2) {  // (an index has at most 20 bits)
+        over = 0;
+        for (int bit = top - 2; bit >= bot; bit -= 2) {  // two bits a step
             const uint32_t one = 1u << bit;
             u64 f[3] = {};
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                f[0] += idx[i] < lo + one ? x[i] : 0;
-                f[1] += idx[i] < lo + 2 * one ? x[i] : 0;
-                f[2] += idx[i] < lo + 3 * one ? x[i] : 0;
+                const u64 x = key[i] > floor ? by_mass ? w[i] : 1 : 0;
+                f[0] += key[i] >= lo + one ? x : 0;
+                f[1] += key[i] >= lo + 2 * one ? x : 0;
+                f[2] += key[i] >= lo + 3 * one ? x : 0;
             }
-            block_sums(f, sh, turn);
-            lo += (f[2] <= goal ? 3u : f[1] <= goal ? 2u : f[0] <= goal ? 1u : 0u) * one;
+            block_sums(f, turn);
+            const int up = f[2] >= need ? 3 : f[1] >= need ? 2 : f[0] >= need ? 1 : 0;
+            lo += up * one;
+            if (up < 3)
+                over = f[up];
         }
         return lo;
-    };
-    uint32_t last_tie = 0xffffffffu;
-    if (ties != ~0ull) {
-        u64 t[PER], c[1] = {};
+    }
+};
+
+// More candidates: the cut's key by bisection.
+__device__ __noinline__ void pick_of_many(const SampleArgs &a, const PickArgs g)
+{
+    int turn = g.turn;
+    ListRegs x;
+    x.load(g.n, g.m, g.inv);
+    uint32_t cut = 0;
+    u64 ties = ~0ull, over;  // tokens at the cut that are kept
+    if (g.k > 0 && g.k < g.n) {
+        cut = x.search(false, (u64)g.k, 0, over, turn);
+        ties = (u64)g.k - over;
+    }
+    if (g.has_p) {
+        u64 c[1] = {};
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            t[i] = key[i] == cut;
-            c[0] += t[i];
+        for (int i = 0; i < ListRegs::PER; ++i)
+            c[0] += x.key[i] > cut ? x.w[i] : 0;
+        block_sums(c, turn);
+        const u64 w_cut = cut ? fixed_mass(expf((key_logit(cut) - g.m) * g.inv)) : 0;
+        const u64 need = needed_mass(g.p, g.k > 0 ? c[0] + (cut ? ties * w_cut : 0) : g.z_all);
+        if (c[0] >= need) {
+            cut = x.search(true, need, cut, over, turn);
+            const u64 w = fixed_mass(expf((key_logit(cut) - g.m) * g.inv));
+            ties = w > 0 ? (need - over + w - 1) / w : 1;
+        } else if (cut && w_cut > 0) {
+            ties = min(ties, (need - c[0] + w_cut - 1) / w_cut);
         }
-        block_sums(c, sh, turn);
-        if (c[0] > ties)
-            last_tie = at_index(t, ties - 1);
     }
-    u64 z[1] = {};
+    // the list is by index: the first ties are kept, and the masses run in its order
+    const uint32_t most = order_key(g.m);
+    u64 mine = 0, all;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool keep = key[i] > cut || (key[i] == cut && idx[i] <= last_tie);
-        if (!keep || (e[i] < mp && key[i] != most))
-            w[i] = 0;
-        z[0] += w[i];
+    for (int i = 0; i < ListRegs::PER; ++i)
+        mine += x.key[i] == cut;
+    u64 tie = ties == ~0ull ? 0 : block_before(mine, all, turn);
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < ListRegs::PER; ++i) {
+        const bool keep = x.key[i] > cut || (x.key[i] == cut && tie < ties);
+        tie += x.key[i] == cut;
+        if (!keep || (x.e[i] < g.mp && x.key[i] != most))
+            x.w[i] = 0;
+        mine += x.w[i];
     }
-    block_sums(z, sh, turn);
-    const u64 goal = goal_mass(u, z[0]);
-    const uint32_t token = at_index(w, goal);
+    u64 z;
+    u64 run = block_before(mine, z, turn);
+    const u64 goal = goal_mass(g.u, z);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (w[i] > 0 && idx[i] == token) {
-            a.tokens[r] = (int)token;
+    for (int i = 0; i < ListRegs::PER; ++i) {
+        if (run <= goal && goal < run + x.w[i]) {
+            a.tokens[g.r] = (int)x.idx[i];
             if (a.probs)
-                a.probs[r] = share(e[i], z[0]);
+                a.probs[g.r] = share(x.e[i], z);
         }
+        run += x.w[i];
+    }
 }
+
+// The tokens left around a cut, as the list: the cut itself (order key,
+// index) to sh.cut.  `need`: the mass or count that they have to reach.
+__device__ __noinline__ void cut_of_list(int n, bool by_mass, u64 need, float m, float inv, int turn)
+{
+    SampleShared &sh = sample_shared();
+    ListRegs x;
+    x.load(n, m, inv);
+    if (by_mass) {
+        // (the mass around the cut was summed over vectors: here the last tokens' may be an ulp of that short)
+        u64 c[1] = {};
+#pragma unroll
+        for (int i = 0; i < ListRegs::PER; ++i)
+            c[0] += x.w[i];
+        block_sums(c, turn);
+        need = min(need, c[0]);
+        if (need == 0) {  // no token here has a mass
+            by_mass = false;
+            need = (u64)n;
+        }
+    }
+    u64 over;
+    const uint32_t cut = x.search(by_mass, need, 0, over, turn);
+    u64 ties = need - over;
+    if (by_mass) {
+        const u64 w = fixed_mass(expf((key_logit(cut) - m) * inv));
+        ties = need > over && w > 0 ? (need - over + w - 1) / w : 1;
+    }
+    u64 mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < ListRegs::PER; ++i)
+        mine += x.key[i] == cut;
+    u64 tie = block_before(mine, all, turn);
+    ties = min(ties, all);
+#pragma unroll
+    for (int i = 0; i < ListRegs::PER; ++i)
+        if (x.key[i] == cut && ++tie == ties)
+            sh.cut = (u64)cut << 32 | x.idx[i];
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- a row
 
 template <typename T>
 struct RowType;
@@ -712,100 +526,527 @@ template <>
 struct RowType<float> {
     static constexpr int E = 4;  // elements of a 16-byte vector
     static constexpr uint32_t LOWEST = 0xff800000u;
+    static __device__ __forceinline__ float at(const uint32_t (&w)[4], int j) { return __uint_as_float(w[j]); }
+    // the larger of two words' elements; NaN against a number gives the number
+    static __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y)
+    {
+        return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+    }
+    static __device__ __forceinline__ float word_max(uint32_t x) { return __uint_as_float(x); }
 };
 template <>
 struct RowType<__nv_bfloat16> {
     static constexpr int E = 8;
     static constexpr uint32_t LOWEST = 0xff80ff80u;
+    static __device__ __forceinline__ float at(const uint32_t (&w)[4], int j)
+    {
+        return (j & 1) ? bf16hi(w[j >> 1]) : bf16lo(w[j >> 1]);
+    }
+    static __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y)
+    {
+        uint32_t z;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+        return z;
+    }
+    static __device__ __forceinline__ float word_max(uint32_t x) { return fmaxf(bf16lo(x), bf16hi(x)); }
 };
 
-// NV vectors of a row in each thread's registers.  A warp's are consecutive:
-// vector v of lane i is the warp's (32 v + i)-th.
+// A thread's vectors of a row, in registers (NV of them) or, with NV = 0,
+// read again in each pass.  A warp's are consecutive: vector v of lane i is
+// the warp's (32 v + i)-th.  Vectors are taken at 16-byte boundaries, so a
+// row may begin and end inside one; elements outside the row, and NaN, are
+// -inf.
 template <typename T, int NV>
-struct RowRegs {
-    static constexpr int E = RowType<T>::E;
-    uint32_t w[NV][4];
+struct Row {
+    typedef RowType<T> R;
+    static constexpr int E = R::E;
+    const T *row;
+    int V, base, per_warp, lane;
+    uint32_t w[NV > 0 ? NV : 1][4];
 
-    __device__ __forceinline__ float at(int v, int j) const
+    __device__ __forceinline__ int index(int v) const { return base + (v * 32 + lane) * E; }
+    __device__ __forceinline__ void read(int v, uint32_t (&q)[4]) const
     {
-        if constexpr (E == 4)
-            return __uint_as_float(w[v][j]);
-        else
-            return (j & 1) ? bf16hi(w[v][j >> 1]) : bf16lo(w[v][j >> 1]);
-    }
-    __device__ __forceinline__ void set(int v, int j, float x)
-    {
-        if constexpr (E == 4) {
-            w[v][j] = __float_as_uint(x);
-        } else {  // (x is a bf16)
-            const uint32_t b = __float_as_uint(x);
-            w[v][j >> 1] = (j & 1) ? (w[v][j >> 1] & 0xffffu) | (b & 0xffff0000u)
-                                   : (w[v][j >> 1] & 0xffff0000u) | (b >> 16);
+        const int i = index(v);
+        const bool mine = v * 32 + lane < per_warp;
+        if (mine && i >= 0 && i + E <= V) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + i));
+            q[0] = R::larger(x.x, R::LOWEST);
+            q[1] = R::larger(x.y, R::LOWEST);
+            q[2] = R::larger(x.z, R::LOWEST);
+            q[3] = R::larger(x.w, R::LOWEST);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = R::LOWEST;
+            if (mine)
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (i + j >= 0 && i + j < V) {
+                        float l = (float)row[i + j];
+                        l = l == l ? l : -INFINITY;
+                        const uint32_t b = __float_as_uint(l);
+                        if constexpr (E == 4)
+                            q[j] = b;
+                        else
+                            q[j >> 1] = (j & 1) ? (q[j >> 1] & 0xffffu) | (b & 0xffff0000u)
+                                                : (q[j >> 1] & 0xffff0000u) | (b >> 16);
+                    }
         }
     }
+    // B vectors from v on; the bounds are looked at once for the whole warp
+    template <int B>
+    __device__ __forceinline__ void read_batch(int v, uint32_t (&q)[B][4]) const
+    {
+        const int i0 = base + v * 32 * E;
+        if (i0 >= 0 && i0 + B * 32 * E <= V && (v + B) * 32 <= per_warp) {
+            const uint4 *at = reinterpret_cast<const uint4 *>(row + i0) + lane;
+            uint4 x[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                x[u] = __ldg(at + u * 32);
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                q[u][0] = R::larger(x[u].x, R::LOWEST);
+                q[u][1] = R::larger(x[u].y, R::LOWEST);
+                q[u][2] = R::larger(x[u].z, R::LOWEST);
+                q[u][3] = R::larger(x[u].w, R::LOWEST);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                read(v + u, q[u]);
+        }
+    }
+    // f(index of the first element, the vector's words) for each vector, in the order of the indices, and after
+    // every fourth, or the last, flush().
+    template <typename F, typename G>
+    __device__ __forceinline__ void each(F &&f, G &&flush) const
+    {
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                f(index(v), w[v]);
+                if (v % 4 == 3 || v == NV - 1)
+                    flush();
+            }
+        } else {
+            constexpr int B = 4;
+            uint32_t q[B][4];
+            for (int v = 0; v * 32 < per_warp; v += B) {
+                read_batch<B>(v, q);
+#pragma unroll
+                for (int u = 0; u < B; ++u)
+                    f(index(v + u), q[u]);
+                flush();
+            }
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F &&f) const
+    {
+        each(f, [] {});
+    }
+    static __device__ __forceinline__ float vector_max(const uint32_t (&q)[4])
+    {
+        return R::word_max(R::larger(R::larger(q[0], q[1]), R::larger(q[2], q[3])));
+    }
+};
+
+// A cut: tokens of larger logits are kept, and those that equal it up to the index.
+struct Cut {
+    float l;
+    int idx;
+    __device__ __forceinline__ bool keeps(float x, int i) const { return x > l || (x == l && i <= idx); }
 };
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(SC_THREADS, 2) k_sample(const SampleArgs a, const int C, const int per_warp)
+struct Sampler {
+    typedef RowType<T> R;
+    static constexpr int E = R::E;
+    Row<T, NV> x;
+    Place &at;
+    float m, inv, c2;
+    __device__ __forceinline__ explicit Sampler(Place &p) : at(p) {}
+
+    __device__ __forceinline__ float e_fast(float l) const { return fast_exp2((l - m) * c2); }  // in sums over many
+
+    // The tokens with keep(logit, index) to rank 0's list, by index.  True
+    // if they fit (n: how many); then only rank 0 may read them, after a
+    // barrier of its own.
+    template <typename P>
+    __device__ __forceinline__ bool gather(float least, int &n, P keep)
+    {
+        SampleShared &sh = sample_shared();
+        const int set = at.turn++ & 1, room = SC_SLOTS / at.C;
+        uint32_t count = 0;
+        auto some = [&](const uint32_t (&q)[4]) { return Row<T, NV>::vector_max(q) >= least; };
+        auto append = [&](int i0, const uint32_t (&q)[4], uint32_t &to, uint32_t end, u64 *slots) {
+            const bool mine = some(q);
+            if (!__any_sync(0xffffffffu, mine))
+                return;
+            uint32_t k = 0;
+            if (mine)
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    k += keep(R::at(q, j), i0 + j);
+            uint32_t inc = k;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (at.lane >= o)
+                    inc += y;
+            }
+            uint32_t p = to + inc - k;
+            to += __shfl_sync(0xffffffffu, inc, 31);
+            if (k)
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float l = R::at(q, j);
+                    if (keep(l, i0 + j)) {
+                        if (p < end) {
+                            const u64 y = (u64)order_key(l + 0.f) << 32 | (uint32_t)(i0 + j);
+                            if (at.C > 1)
+                                st_cluster(&slots[p], 0u, y);
+                            else
+                                slots[p] = y;
+                        }
+                        ++p;
+                    }
+                }
+        };
+        if constexpr (NV > 0) {
+            // count, then place: the warps' before this one's
+            uint32_t k = 0;
+            x.each([&](int i0, const uint32_t(&q)[4]) {
+                if (some(q))
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        k += keep(R::at(q, j), i0 + j);
+            });
+            k = __reduce_add_sync(0xffffffffu, k);
+            if (at.lane == 0)
+                sh.warp32[at.warp] = k;
+            __syncthreads();
+            const uint32_t w = at.lane < SC_WARPS ? sh.warp32[at.lane] : 0u;
+            count = __reduce_add_sync(0xffffffffu, w);
+            if (k) {
+                uint32_t to = __reduce_add_sync(0xffffffffu, at.lane < at.warp ? w : 0u);
+                x.each([&](int i0, const uint32_t(&q)[4]) {
+                    append(i0, q, to, (uint32_t)room, sh.slots + at.rank * room);
+                });
+            }
+            __syncthreads();
+            if (threadIdx.x < at.C)
+                st_cluster(&sh.x64[set][0][at.rank], threadIdx.x, (u64)count);
+            at.barrier();
+            u64 all = 0;
+            bool fits = true;
+            for (int q = 0; q < at.C; ++q) {
+                const u64 nq = sh.x64[set][0][q];
+                all += nq;
+                fits = fits && nq <= (u64)room;
+            }
+            n = (int)all;
+            if (!fits || all > SC_LIST)
+                return false;
+            if (at.rank == 0 && at.warp < at.C) {  // in a row: a warp per CTA's share
+                int to = 0;
+                for (int q = 0; q < at.warp; ++q)
+                    to += (int)sh.x64[set][0][q];
+                const int nq = (int)sh.x64[set][0][at.warp];
+                for (int i = at.lane; i < nq; i += 32)
+                    sh.list[to + i] = sh.slots[at.warp * room + i];
+            }
+        } else {
+            // (C = 1) one pass: each warp places at its own share of the slots
+            constexpr uint32_t SHARE = SC_SLOTS / SC_WARPS;
+            __syncthreads();  // the slots' last readers
+            x.each([&](int i0, const uint32_t(&q)[4]) { append(i0, q, count, SHARE, sh.slots + at.warp * SHARE); });
+            if (at.lane == 0)
+                sh.part[set][0][at.warp] = count;
+            __syncthreads();
+            const uint32_t w = at.lane < SC_WARPS ? (uint32_t)sh.part[set][0][at.lane] : 0u;
+            n = (int)__reduce_add_sync(0xffffffffu, w);
+            if (__reduce_max_sync(0xffffffffu, w) > SHARE || n > SC_LIST)
+                return false;
+            const uint32_t to = __reduce_add_sync(0xffffffffu, at.lane < at.warp ? w : 0u);
+            for (uint32_t i = at.lane; i < count; i += 32)
+                sh.list[to + i] = sh.slots[at.warp * SHARE + i];
+        }
+        return true;
+    }
+
+    // Thresholds about the cut, from a sample of the row (with NV = 0, where
+    // a pass over all of it is dear): 16 elements a thread, evenly spread.
+    // Narrows until 1.5 standard errors of the sample's share lie between.
+    __device__ __forceinline__ void guess(bool by_mass, float part, const Cut in, float (&t)[3])
+    {
+        constexpr int SV = 16 / E;
+        uint32_t q[SV][4];
+        const int apart = max(1, (x.per_warp + 31) / 32 / SV);
+#pragma unroll
+        for (int i = 0; i < SV; ++i)
+            x.read(i * apart, q[i]);
+        u64 none[1] = {};
+        cluster_sums(none, at);  // (its barrier: the sums below use the same words)
+        float a = 0.f, b = 0.f;
+        u64 all = 0, f_a = 0, f_b = 0;
+        for (int step = 0; step < 10; ++step) {
+            if (step == 1) {  // from the least token on; where that is -inf or far off, what has a mass
+                a = m - 30.f / c2;
+                if (!(a > -INFINITY))
+                    return;
+                b = m;
+            }
+            const float w = (b - a) * 0.25f;
+            const float c[3] = {step ? a + w : -INFINITY, a + 2.f * w, a + 3.f * w};
+            u64 s[3] = {};
+#pragma unroll
+            for (int i = 0; i < SV; ++i) {
+                float f0 = 0.f, f1 = 0.f, f2 = 0.f;
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float l = R::at(q[i], j);
+                    const float e = in.keeps(l, x.index(i * apart) + j) ? by_mass ? e_fast(l) : 1.f : 0.f;
+                    f0 += l >= c[0] ? e : 0.f;
+                    f1 += l >= c[1] ? e : 0.f;
+                    f2 += l >= c[2] ? e : 0.f;
+                }
+                s[0] += fixed_mass(f0);
+                s[1] += fixed_mass(f1);
+                s[2] += fixed_mass(f2);
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                s[i] = warp_sum64(s[i]);
+            cluster_sums(s, at);
+            if (step == 0) {
+                all = f_a = s[0];
+                f_b = 0;
+                continue;
+            }
+            const u64 want = (u64)(__ull2float_rn(all) * part);
+            const int up = s[2] >= want ? 3 : s[1] >= want ? 2 : s[0] >= want ? 1 : 0;
+            f_a = up ? s[up - 1] : f_a;
+            f_b = up < 3 ? s[up] : f_b;
+            b = up < 3 ? c[up] : b;
+            a = up ? c[up - 1] : a;
+            if (f_a - f_b <= (all >> 7))
+                break;
+        }
+        t[0] = a - (b - a);
+        t[1] = 0.5f * (a + b);
+        t[2] = b + (b - a);
+    }
+
+    // The cut that `need` of the mass (or of the tokens) kept by `in`
+    // reaches; all of them, `total`, reach it.
+    __device__ __noinline__ Cut search(bool by_mass, u64 need, u64 total, const Cut in)
+    {
+        SampleShared &sh = sample_shared();
+        // (in registers a pass is cheap: some multiples of the temperature below the maximum)
+        float first[3] = {m - 16.f / c2, m - 8.f / c2, m - 4.f / c2};
+        if (NV == 0)
+            guess(by_mass, __ull2float_rn(need) / __ull2float_rn(total), in, first);
+        // what is at or above a reaches it, what is at or above b does not
+        uint32_t a = max(order_key(in.l), KEY_LOWEST + 1), b = order_key(m) + 1;
+        u64 over = 0, n_over = 0, n_a = ~0ull;  // at or above b: mass or count, and count; count at or above a
+        for (int step = 0; b - a > 1; ++step) {
+            // three thresholds between: the guess; where it missed, close by; then by turns evenly in the logits, which halves the tokens of a smooth
+            // distribution soonest, and evenly in the keys, which ends
+            uint32_t t[3];
+            const float la = key_logit(a), lb = key_logit(b - 1);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                t[i] = a + (uint32_t)(((u64)(b - a) * (i + 1)) >> 2);
+                if (step == 0 && first[i] > -INFINITY)
+                    t[i] = order_key(first[i] + 0.f);
+                else if (NV == 0 && step == 1 && a == order_key(first[2] + 0.f))
+                    t[i] = order_key(first[2] + (first[2] - first[1]) * (i == 0 ? 1.f : i == 1 ? 3.f : 8.f) + 0.f);
+                else if (NV == 0 && step == 1 && b == order_key(first[0] + 0.f))
+                    t[i] = order_key(first[0] - (first[2] - first[1]) * (i == 0 ? 8.f : i == 1 ? 3.f : 1.f) + 0.f);
+                else if (!(step & 1) && la > -INFINITY && lb < INFINITY)
+                    t[i] = order_key(la + (lb - la) * (0.25f * (i + 1)) + 0.f);
+                t[i] = min(max(t[i], a + 1), b - 1);
+            }
+            const float f0 = key_logit(t[0]), f1 = key_logit(t[1]), f2 = key_logit(t[2]);
+            u64 s[4] = {};
+            // (masks of 0 and 1: a set, a fused product and a sum for each threshold)
+            float m0 = 0.f, m1 = 0.f, m2 = 0.f, c0 = 0.f, c1 = 0.f, c2_ = 0.f;
+            auto pass = [&](auto all) {
+                x.each(
+                    [&](int i0, const uint32_t(&q)[4]) {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            const float l =
+                                decltype(all)::value || in.keeps(R::at(q, j), i0 + j) ? R::at(q, j) : -INFINITY;
+                            const float k0 = l >= f0 ? 1.f : 0.f, k1 = l >= f1 ? 1.f : 0.f, k2 = l >= f2 ? 1.f : 0.f;
+                            if (by_mass) {
+                                const float e = e_fast(l);
+                                m0 = fmaf(e, k0, m0);
+                                m1 = fmaf(e, k1, m1);
+                                m2 = fmaf(e, k2, m2);
+                            }
+                            c0 += k0;
+                            c1 += k1;
+                            c2_ += k2;
+                        }
+                    },
+                    [&] {
+                        if (by_mass) {
+                            s[0] += fixed_mass(m0);
+                            s[1] += fixed_mass(m1);
+                            s[2] += fixed_mass(m2);
+                            m0 = m1 = m2 = 0.f;
+                        }
+                    });
+            };
+            if (in.l == -INFINITY)
+                pass(std::true_type{});
+            else
+                pass(std::false_type{});
+            // (a thread's counts are exact: below 2^24)
+            const uint32_t n0 = __reduce_add_sync(0xffffffffu, __float2uint_rz(c0));
+            const uint32_t n1 = __reduce_add_sync(0xffffffffu, __float2uint_rz(c1));
+            const uint32_t n2 = __reduce_add_sync(0xffffffffu, __float2uint_rz(c2_));
+            s[0] = warp_sum64(s[0]);
+            s[1] = warp_sum64(s[1]);
+            s[2] = warp_sum64(s[2]);
+            s[3] = (u64)n0 | (u64)n1 << 21 | (u64)n2 << 42;
+            cluster_sums(s, at);
+            const u64 n[3] = {s[3] & 0x1fffffu, (s[3] >> 21) & 0x1fffffu, s[3] >> 42};
+            // (in equal thresholds the later ones change nothing)
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {
+                const u64 f = by_mass ? s[i] : n[i];
+                if (f >= need) {
+                    if (t[i] > a) {
+                        a = t[i];
+                        n_a = n[i];
+                    }
+                } else if (t[i] < b) {
+                    b = t[i];
+                    over = f;
+                    n_over = n[i];
+                }
+            }
+            if (n_a - n_over <= SC_LIST && b - a > 1) {
+                // few enough around the cut for one CTA
+                const float fa = key_logit(a), fb = key_logit(b);
+                int n_list;
+                const bool fits = gather(fa, n_list, [&](float l, int i) {
+                    return l >= fa && !(l >= fb) && in.keeps(l, i);
+                });
+                if (fits && n_list > 0) {
+                    const int set = at.turn++ & 1;
+                    if (at.rank == 0) {
+                        __syncthreads();
+                        cut_of_list(n_list, by_mass, need - over, m, inv, at.turn);
+                        if (threadIdx.x < at.C)
+                            st_cluster(&sh.x64[set][1][0], threadIdx.x, sh.cut);
+                    }
+                    at.barrier();
+                    const u64 cut = sh.x64[set][1][0];
+                    at.turn += 64;  // (rank 0 went on from here in the CTA's own exchanges)
+                    at.barrier();
+                    return Cut{key_logit((uint32_t)(cut >> 32)), (int)(uint32_t)cut};
+                }
+                n_a = ~0ull;  // (no place for them: on to a single value)
+            }
+        }
+        // a single value: its first tokens by index
+        const float l = key_logit(a);
+        u64 ties = need - over;
+        if (by_mass) {
+            const u64 w = fixed_mass(e_fast(l));
+            ties = need > over && w > 0 ? (need - over + w - 1) / w : 1;
+        }
+        uint32_t k = 0;
+        x.each([&](int i0, const uint32_t(&q)[4]) {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                k += R::at(q, j) == l && in.keeps(l, i0 + j);
+        });
+        k = __reduce_add_sync(0xffffffffu, k);
+        u64 all;
+        u64 run = cluster_before(k, all, at);
+        uint32_t found = 0;
+        if (all > ties && run < ties && ties <= run + k)
+            x.each([&](int i0, const uint32_t(&q)[4]) {
+                uint32_t mine = 0;
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    mine += R::at(q, j) == l && in.keeps(l, i0 + j);
+                uint32_t inc = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (at.lane >= o)
+                        inc += y;
+                }
+                u64 p = run + inc - mine;
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (R::at(q, j) == l && in.keeps(l, i0 + j) && ++p == ties)
+                        found = (uint32_t)(i0 + j) + 1;
+                run += __shfl_sync(0xffffffffu, inc, 31);
+            });
+        u64 s[1] = {__reduce_add_sync(0xffffffffu, found)};
+        cluster_sums(s, at);
+        return Cut{l, s[0] ? (int)s[0] - 1 : l == in.l ? in.idx : 0x7fffffff};
+    }
+};
+
+// A row that the first kernel leaves to the second gets a token of PENDING or
+// less: PENDING less a number that spreads such rows over the second one's
+// clusters (a count that is never reset: any number will do).
+constexpr int PENDING = -2;
+__device__ unsigned g_pending;
+
+// One row.  defer: where the cut needs a search, the row is left pending.
+template <typename T, int NV>
+__device__ __forceinline__ void sample_row(const SampleArgs &a, Place &at, int per_warp, int r, bool defer)
 {
-    constexpr int E = RowType<T>::E;
+    typedef RowType<T> R;
+    constexpr int E = R::E;
     SampleShared &sh = sample_shared();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = C > 1 ? cluster_ctarank() : 0;
-    if (C > 1)  // (waited for before the first access to another CTA's shared memory: all have begun)
+    Sampler<T, NV> y(at);
+    Row<T, NV> &x = y.x;
+    const int tid = threadIdx.x, lane = at.lane, warp = at.warp;
+    // (waited for before the first access to another CTA's shared memory: all have begun, and ended the row before)
+    if (at.C > 1)
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    const int r = blockIdx.x / C, V = a.V;
-    const T *row = static_cast<const T *>(a.logits) + r * a.stride;
-    // vectors are taken at 16-byte boundaries: `head` elements of the first lie before the row
-    const int head = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    // every warp of the cluster has per_warp vectors, so that the CTAs' shares are alike
-    const int base = ((int)rank * SC_WARPS + warp) * per_warp * E - head;  // index of the warp's first element
-    auto index = [&](int v, int j) { return base + (v * 32 + lane) * E + j; };
-    int turn = 0;
+    const int V = a.V;
     // the row's settings are on their way with its logits
     const float tau = a.tau ? a.tau[r] : 1.f;
     const int k = a.top_k ? a.top_k[r] : 0;
     const float p = a.top_p ? a.top_p[r] : 1.f;
     const float mp_given = a.min_p ? a.min_p[r] : 0.f;
     const float u = a.u[r];
+    x.row = static_cast<const T *>(a.logits) + r * a.stride;
+    x.V = V;
+    x.lane = lane;
+    x.per_warp = per_warp;  // of every warp of the cluster, so that the CTAs' shares are alike
+    x.base = ((int)at.rank * SC_WARPS + warp) * per_warp * E -
+             (int)((reinterpret_cast<uintptr_t>(x.row) & 15u) / sizeof(T));
+    if constexpr (NV > 0)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            x.read(v, x.w[v]);
+    uint32_t top2 = R::LOWEST;
+    x.each([&](int, const uint32_t(&q)[4]) {
+        top2 = R::larger(top2, R::larger(R::larger(q[0], q[1]), R::larger(q[2], q[3])));
+    });
+    const float my_max = R::word_max(top2) + 0.f;  // (-0 counts as 0)
+    const bool has_k = k > 0 && k < V, has_p = p < 1.f;
 
-    RowRegs<T, NV> x;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = index(v, 0);
-        if (i >= 0 && i + E <= V && v * 32 + lane < per_warp) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + i));
-            x.w[v][0] = q.x;
-            x.w[v][1] = q.y;
-            x.w[v][2] = q.z;
-            x.w[v][3] = q.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x.w[v][j] = RowType<T>::LOWEST;
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (i + j >= 0 && i + j < V && v * 32 + lane < per_warp)
-                    x.set(v, j, (float)row[i + j]);
-        }
-    }
-    // NaN counts as -inf, -0 as 0
-    float m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float l = x.at(v, j) + 0.f;
-            l = l == l ? l : -INFINITY;
-            x.set(v, j, l);
-            m = fmaxf(m, l);
-        }
-    const float my_max = m;
-    const bool has_k = k > 0 && k < V;
-    uint32_t k_key = 0;  // an order key that at least k tokens reach
+    // ---- the maximum, and with a top-k an order key that at least k tokens reach
+    uint32_t k_key = 0;
+    float m;
     {
         const uint32_t mine = order_key(my_max);
-        const int want = (k + C - 1) / C;
+        const int want = (k + at.C - 1) / at.C;
         if (has_k && want <= SC_THREADS) {
             // At least k / C (rounded up) of this CTA's tokens reach the threads' maximum of that rank, so at least k
             // of all reach the least of the CTAs' ones.  Two bits a step: the threads that reach each of three
@@ -830,56 +1071,53 @@ __global__ void __launch_bounds__(SC_THREADS, 2) k_sample(const SampleArgs a, co
         if (lane == 0)
             sh.warp32[warp] = top;
         __syncthreads();
-        if (C > 1)
+        top = __reduce_max_sync(0xffffffffu, lane < SC_WARPS ? sh.warp32[lane] : 0u);
+        if (at.C > 1) {
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (warp == 0) {
-            top = __reduce_max_sync(0xffffffffu, lane < SC_WARPS ? sh.warp32[lane] : 0u);
-            if (lane < C)
-                st_cluster(&sh.x64[1][7][rank], (uint32_t)lane, (u64)top << 32 | k_key);
-        }
-        if (C > 1)
+            if (tid < at.C)
+                st_cluster(&sh.x64[1][7][at.rank], (uint32_t)tid, (u64)top << 32 | k_key);
             cluster_sync();
-        else
-            __syncthreads();
-        top = 0;
-        for (int q = 0; q < C; ++q) {
-            top = max(top, (uint32_t)(sh.x64[1][7][q] >> 32));
-            k_key = min(k_key, (uint32_t)sh.x64[1][7][q]);
+            for (int q = 0; q < at.C; ++q) {
+                top = max(top, (uint32_t)(sh.x64[1][7][q] >> 32));
+                k_key = min(k_key, (uint32_t)sh.x64[1][7][q]);
+            }
+        } else {
+            __syncthreads();  // (warp32 is used again)
         }
         m = key_logit(top);
     }
     if (m == -INFINITY) {
-        if (rank == 0 && tid == 0) {
+        if (at.rank == 0 && tid == 0) {
             a.tokens[r] = -1;
             if (a.probs)
                 a.probs[r] = 0.f;
         }
-        return;  // (the whole cluster; its last DSMEM access was before the barrier)
+        return;  // (the whole cluster; its last access to another's shared memory was before the barrier)
     }
     if (!(tau > 0.f)) {  // the largest, of the lowest index
         uint32_t best = 0xffffffffu;
+        if (my_max == m)
+            x.each([&](int i0, const uint32_t(&q)[4]) {
+                if (Row<T, NV>::vector_max(q) == m)
 #pragma unroll
-        for (int v = NV - 1; v >= 0; --v)
-#pragma unroll
-            for (int j = E - 1; j >= 0; --j)
-                if (x.at(v, j) == m)
-                    best = (uint32_t)index(v, j);
+                    for (int j = E - 1; j >= 0; --j)
+                        if (R::at(q, j) == m)
+                            best = min(best, (uint32_t)(i0 + j));
+            });
         best = __reduce_min_sync(0xffffffffu, best);
         if (lane == 0)
             sh.warp32[warp] = best;
         __syncthreads();
-        if (warp == 0) {
-            best = __reduce_min_sync(0xffffffffu, lane < SC_WARPS ? sh.warp32[lane] : 0xffffffffu);
-            if (lane == 0)
-                st_cluster(&sh.x64[0][7][rank], 0u, (u64)best);
-        }
-        if (C > 1)
+        best = __reduce_min_sync(0xffffffffu, lane < SC_WARPS ? sh.warp32[lane] : 0xffffffffu);
+        if (at.C > 1) {
+            if (tid == 0)
+                st_cluster(&sh.x64[0][7][at.rank], 0u, (u64)best);
             cluster_sync();
-        else
-            __syncthreads();
-        if (rank == 0 && tid == 0) {
-            for (int q = 0; q < C; ++q)
-                best = min(best, (uint32_t)sh.x64[0][7][q]);
+            if (at.rank == 0)
+                for (int q = 0; q < at.C; ++q)
+                    best = min(best, (uint32_t)sh.x64[0][7][q]);
+        }
+        if (at.rank == 0 && tid == 0) {
             a.tokens[r] = (int)best;
             if (a.probs)
                 a.probs[r] = 1.f;
@@ -887,52 +1125,93 @@ __global__ void __launch_bounds__(SC_THREADS, 2) k_sample(const SampleArgs a, co
         return;
     }
     // (a temperature beyond 1e37 or below 1e-37 counts as that: no product below is inf * 0)
-    const float inv = fminf(fmaxf(1.f / tau, 1e-37f), 1e37f), c2 = inv * 1.44269504088896341f;
-    float tmax = my_max;
-    const bool inf_row = m == INFINITY;
-    if (inf_row) {  // the tokens at +inf share the mass
-        tmax = my_max == INFINITY ? 0.f : -INFINITY;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
+    const float inv = fminf(fmaxf(1.f / tau, 1e-37f), 1e37f);
+    const float mp = mp_given > 0.f ? fminf(mp_given, 1.f) : 0.f;
+    const bool inf_row = m == INFINITY;  // the tokens at inf share the mass: all others' is 0
+    y.m = m;
+    y.inv = inv;
+    y.c2 = inv * 1.44269504088896341f;
+    if (inf_row) {
+        // Any m between works: tokens at inf get e = inf, cut to 1 in sums -- simplest is to take them by index.
+        // The first `keep` of them (a top-k, then a top-p, of equal masses) share the mass.
+        uint32_t n = 0;
+        x.each([&](int, const uint32_t(&q)[4]) {
 #pragma unroll
             for (int j = 0; j < E; ++j)
-                x.set(v, j, x.at(v, j) == INFINITY ? 0.f : -INFINITY);
-        m = 0.f;
+                n += R::at(q, j) == INFINITY;
+        });
+        n = __reduce_add_sync(0xffffffffu, n);
+        u64 all;
+        u64 run = cluster_before(n, all, at);
+        u64 keep = has_k ? min(all, (u64)k) : all;
+        if (has_p) {
+            const u64 one = 1ull << 40;
+            keep = min(keep, (needed_mass(p, keep * one) + one - 1) / one);
+        }
+        const u64 pick = goal_mass(u, keep << 40) >> 40;
+        if (run <= pick && pick < run + n)
+            x.each([&](int i0, const uint32_t(&q)[4]) {
+                uint32_t mine = 0;
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    mine += R::at(q, j) == INFINITY;
+                uint32_t inc = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t z = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o)
+                        inc += z;
+                }
+                u64 q0 = run + inc - mine;
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (R::at(q, j) == INFINITY && q0++ == pick) {
+                        a.tokens[r] = i0 + j;
+                        if (a.probs)
+                            a.probs[r] = 1.f / (float)keep;
+                    }
+                run += __shfl_sync(0xffffffffu, inc, 31);
+            });
+        return;
     }
-    const float mp = mp_given > 0.f ? fminf(mp_given, 1.f) : 0.f;
-    const bool has_p = p < 1.f;
-    auto e_of = [&](float l) { return expf((l - m) * inv); };           // of a single token
-    auto e_fast = [&](float l) { return fast_exp2((l - m) * c2); };     // in sums over many
     // below this no token has e >= min_p (with room for the roundings)
     const float l_mp = mp > 0.f ? m + (logf(mp) - 1e-3f) * (1.f / inv) : -INFINITY;
 
-    // ---- the bound and, where it is needed, the mass of all
+    // ---- the bound and, for a top-p of all tokens, their mass
     float bound = -INFINITY;
     u64 z_all = 0;
-    bool listed = false;  // the candidates fit the list
+    bool listed = false;  // the bound is worth a try
     if (has_k) {
-        // (with m = inf its tokens alone have mass; a key below -inf's is no float)
-        bound = inf_row || k_key <= order_key(-INFINITY) ? -INFINITY : key_logit(k_key);
+        bound = k_key <= KEY_LOWEST ? -INFINITY : key_logit(k_key);  // (a key below -inf's is no float)
         if (!has_p)
             bound = fmaxf(bound, l_mp);
         listed = true;
     } else if (has_p) {
-        const float b0 = m - 8.f / c2, b1 = m - 14.f / c2, b2 = m - 20.f / c2;
-        u64 s[1 + SC_TRIALS] = {};  // the mass, and that above each bound
-        float t0 = 0.f, t1 = 0.f, t2 = 0.f;
+        // trial bounds: e >= 2^-8, 2^-14, 2^-20
+        const float b0 = m - 8.f / y.c2, b1 = m - 14.f / y.c2, b2 = m - 20.f / y.c2;
+        u64 s[5] = {};  // the mass, that above each bound, the tokens above them
+        float t = 0.f, t0 = 0.f, t1 = 0.f, t2 = 0.f, n0 = 0.f, n1 = 0.f, n2 = 0.f;
+        x.each(
+            [&](int, const uint32_t(&q)[4]) {
+                float v = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float t = 0.f;
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float l = x.at(v, j), e = e_fast(l);
-                t += e;
-                t0 += l >= b0 ? e : 0.f;
-                t1 += l >= b1 ? e : 0.f;
-                t2 += l >= b2 ? e : 0.f;
-            }
-            s[0] += fixed_mass(t);
-        }
+                for (int j = 0; j < E; ++j) {
+                    const float l = R::at(q, j), e = y.e_fast(l);
+                    const float k0 = l >= b0 ? 1.f : 0.f, k1 = l >= b1 ? 1.f : 0.f, k2 = l >= b2 ? 1.f : 0.f;
+                    v += e;
+                    t0 = fmaf(e, k0, t0);
+                    t1 = fmaf(e, k1, t1);
+                    t2 = fmaf(e, k2, t2);
+                    n0 += k0;
+                    n1 += k1;
+                    n2 += k2;
+                }
+                t += v;
+            },
+            [&] {
+                s[0] += fixed_mass(t);
+                t = 0.f;
+            });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             t0 += __shfl_xor_sync(0xffffffffu, t0, o);
@@ -943,340 +1222,253 @@ __global__ void __launch_bounds__(SC_THREADS, 2) k_sample(const SampleArgs a, co
         s[1] = fixed_mass(t0);
         s[2] = fixed_mass(t1);
         s[3] = fixed_mass(t2);
-        cluster_sums<true>(s, sh, turn, C, rank);
+        s[4] = (u64)__reduce_add_sync(0xffffffffu, __float2uint_rz(n0)) |
+               (u64)__reduce_add_sync(0xffffffffu, __float2uint_rz(n1)) << 21 |
+               (u64)__reduce_add_sync(0xffffffffu, __float2uint_rz(n2)) << 42;
+        cluster_sums(s, at);
         z_all = s[0];
-        // (the trial masses are good to 1e-6; a bound that only just suffices is passed over)
-        const u64 need = needed_mass(p, z_all), more = need + (need >> 16);
-        const float b[SC_TRIALS] = {b0, b1, b2};
-        for (int i = SC_TRIALS - 1; i >= 0; --i)
-            if (s[1 + i] >= more) {
-                bound = b[i];
-                listed = true;  // (unless they are too many, as it turns out)
-            }
-        if (mp > 0.f)
-            listed = true;  // as far as min_p goes
+        // (the trial masses are good to 1e-5; a bound that only just suffices is passed over)
+        const u64 need = needed_mass(p, z_all), more = need + (need >> 15);
+        const int i = s[1] >= more ? 0 : s[2] >= more ? 1 : s[3] >= more ? 2 : 3;
+        bound = i == 0 ? b0 : i == 1 ? b1 : i == 2 ? b2 : -INFINITY;
+        // (a bound from min_p may leave fewer)
+        listed = (i < 3 && ((s[4] >> (21 * i)) & 0x1fffffu) <= SC_LIST) || l_mp > bound;
         bound = fmaxf(bound, l_mp);
     }
-
-    // ---- the candidates at or above the bound, to rank 0
+    // ---- the candidates at or above the bound
     if (listed) {
-        const int set = turn++ & 1;
-        if (tid == 0)
-            sh.count = 0;
-        __syncthreads();
-        const int room = SC_SLOTS / C;
-        if (tmax >= bound)  // (few threads hold a candidate)
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float l = x.at(v, j);
-                    if (l >= bound && l > -INFINITY) {
-                        const uint32_t at = atomicAdd(&sh.count, 1u);
-                        if (at < (uint32_t)room)
-                            st_cluster(&sh.slots[rank * room + at], 0u,
-                                       ((u64)~order_key(l) << 32) | (uint32_t)index(v, j));
-                    }
-                }
-        __syncthreads();
-        if (tid < C)
-            st_cluster(&sh.x64[set][0][rank], (uint32_t)tid, (u64)sh.count);
-        if (C > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        u64 n_all = 0;
-        bool fits = true;
-        for (int q = 0; q < C; ++q) {
-            n_all += sh.x64[set][0][q];
-            fits = fits && sh.x64[set][0][q] <= (u64)room;
-        }
-        if (fits && n_all <= SC_LIST) {
-            if (rank != 0)
+        int n;
+        if (y.gather(bound, n, [&](float l, int) { return l >= bound && l > -INFINITY; })) {
+            if (at.rank != 0)
                 return;
-            // in a row: a warp per CTA's share
-            if (warp < C) {
-                int at = 0;
-                for (int q = 0; q < warp; ++q)
-                    at += (int)sh.x64[set][0][q];
-                const int nq = (int)sh.x64[set][0][warp];
-                for (int i = lane; i < nq; i += 32)
-                    sh.list[at + i] = sh.slots[warp * room + i];
-            }
             __syncthreads();
-            const int n = (int)n_all, kk = has_k ? k : 0;
+            const PickArgs g{r, n, has_k ? k : 0, has_p, p, mp, u, m, inv, z_all, at.turn};
             if (n <= SC_THREADS / 8)
-                pick_by_counting<8>(a, r, n, kk, has_p, p, mp, u, m, inv, z_all);
-            else if (n <= SC_THREADS / 2)
-                pick_by_counting<2>(a, r, n, kk, has_p, p, mp, u, m, inv, z_all);
-            else if (n <= SC_THREADS)
-                pick_by_counting<1>(a, r, n, kk, has_p, p, mp, u, m, inv, z_all);
+                pick_of_few<8>(a, g);
+            else if (n <= SC_FEW)
+                pick_of_few<2>(a, g);
             else
-                pick_by_bisection(a, r, n, kk, has_p, p, mp, u, m, inv, z_all);
+                pick_of_many(a, g);
             return;
         }
     }
-
-    // ---- too many candidates, or no bound at all: the cut by bisection over the registers
-    uint32_t cut = 0;    // order key of the last kept logit
-    u64 ties = ~0ull;    // how many of the tokens that equal it are kept, by index
-    u64 above = 0;       // mass of the tokens above it
-    auto key_at = [&](int v, int j) { return order_key(x.at(v, j)); };
-    // the logit from which on a token's key is at least t (keys below -inf's and above inf's are no floats)
-    auto threshold = [&](uint32_t t) { return t <= order_key(-INFINITY) ? -INFINITY : key_logit(t); };
-    if (has_k) {
-        uint32_t lo = 0;  // the largest key with at least k tokens at or above
-        for (int bit = 30; bit >= (E == 8 ? 16 : 0); bit -= 2) {  // two bits a step
-            const uint32_t one = 1u << bit;
-            const float f0 = threshold(lo + one), f1 = threshold(lo + 2 * one), f2 = threshold(lo + 3 * one);
-            uint32_t n0 = 0, n1 = 0, n2 = 0;
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float l = x.at(v, j);
-                    n0 += l >= f0;
-                    n1 += l >= f1;
-                    n2 += l >= f2;
-                }
-            n0 = __reduce_add_sync(0xffffffffu, n0);
-            n1 = __reduce_add_sync(0xffffffffu, n1);
-            n2 = __reduce_add_sync(0xffffffffu, n2);
-            u64 s[1] = {(u64)n0 | (u64)n1 << 21 | (u64)n2 << 42};
-            cluster_sums<true>(s, sh, turn, C, rank);
-            const uint32_t q0 = s[0] & 0x1fffffu, q1 = (s[0] >> 21) & 0x1fffffu, q2 = s[0] >> 42;
-            lo += one * (q2 >= (uint32_t)k ? 3u : q1 >= (uint32_t)k ? 2u : q0 >= (uint32_t)k ? 1u : 0u);
-        }
-        cut = lo;
-        if (E == 8 && !(lo >> 31))
-            cut |= 0xffffu;  // a negative bf16's key ends in ones
+    // ---- too many, or no bound: the cut by search, then the kept masses in index order
+    if (defer && (has_k || has_p)) {
+        if (tid == 0)
+            a.tokens[r] = PENDING - (int)(atomicAdd(&g_pending, 1u) & 0xffffu);
+        return;
     }
-    if (has_k) {
-        // mass above the cut, tokens above and at it
-        u64 s[3] = {};
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
+    Cut cut{-INFINITY, -0x7fffffff};
+    auto mass_of = [&](const Cut &c) {
+        u64 s[1] = {};
+        x.each([&](int i0, const uint32_t(&q)[4]) {
             float t = 0.f;
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const uint32_t key = key_at(v, j);
-                if (key > cut) {
-                    t += e_fast(x.at(v, j));
-                    ++s[1];
-                }
-                s[2] += key == cut;
-            }
+            for (int j = 0; j < E; ++j)
+                t += c.keeps(R::at(q, j), i0 + j) ? y.e_fast(R::at(q, j)) : 0.f;
             s[0] += fixed_mass(t);
-        }
-        cluster_sums<false>(s, sh, turn, C, rank);
-        above = s[0];
-        ties = min(s[2], (u64)k - s[1]);
-    }
-    const u64 w_cut = cut ? fixed_mass(e_of(key_logit(cut))) : 0;
-    if (has_p) {
-        const u64 zk = has_k ? above + ties * w_cut : z_all;
-        const u64 need = needed_mass(p, zk);
-        if (above >= need || !has_k) {  // the cut moves up: the largest key with at least `need` at or above
-            uint32_t lo = 0;
-            u64 over = 0;  // mass above it
-            const float cut_l = cut ? key_logit(cut) : -INFINITY;  // (a token at -inf has no mass)
-            for (int bit = 30; bit >= (E == 8 ? 16 : 0); bit -= 2) {  // two bits a step
-                const uint32_t one = 1u << bit;
-                const float f0 = threshold(lo + one), f1 = threshold(lo + 2 * one), f2 = threshold(lo + 3 * one);
-                u64 s[3] = {};
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    float t0 = 0.f, t1 = 0.f, t2 = 0.f;
-#pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        const float l = x.at(v, j), e = l > cut_l ? e_fast(l) : 0.f;
-                        t0 += l >= f0 ? e : 0.f;
-                        t1 += l >= f1 ? e : 0.f;
-                        t2 += l >= f2 ? e : 0.f;
-                    }
-                    s[0] += fixed_mass(t0);
-                    s[1] += fixed_mass(t1);
-                    s[2] += fixed_mass(t2);
-                }
-                cluster_sums<false>(s, sh, turn, C, rank);
-                const uint32_t up = s[2] >= need ? 3u : s[1] >= need ? 2u : s[0] >= need ? 1u : 0u;
-                lo += up * one;
-                if (up < 3)
-                    over = s[up];  // the least threshold that falls short
-            }
-            if (E == 8 && !(lo >> 31))
-                lo |= 0xffffu;
-            cut = max(lo, cut);
-            const u64 w = fixed_mass(e_of(key_logit(cut)));
-            ties = w > 0 && need > over ? (need - over + w - 1) / w : 1;
-        } else if (w_cut > 0) {
-            ties = min(ties, (need - above + w_cut - 1) / w_cut);
-        }
-    }
-    // the kept masses in index order: a vector's in turn, a lane's vectors of a warp 32 apart
-    int last_tie = V;
-    if (ties != ~0ull) {
-        // the index of the last tie kept
-        u64 n = 0;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
+        });
+        s[0] = warp_sum64(s[0]);
+        return s[0];
+    };
+    if (has_k) {
+        // (fewer than k tokens above -inf: all of them)
+        uint32_t n = 0;
+        x.each([&](int, const uint32_t(&q)[4]) {
 #pragma unroll
             for (int j = 0; j < E; ++j)
-                n += key_at(v, j) == cut;
-        // (within a warp the order is vector by vector, so the warp's first lane counts for all of it)
-        const u64 in_warp = warp_sum64(n);
-        u64 all;
-        const u64 before = __shfl_sync(0xffffffffu, cluster_before(lane == 0 ? in_warp : 0, all, sh, turn, C, rank), 0);
-        uint32_t found = 0xffffffffu;
-        if (all > ties && before < ties && ties <= before + in_warp) {
-            u64 run = before;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                int mine = 0;
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    mine += key_at(v, j) == cut;
-                int inc = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o)
-                        inc += y;
-                }
-                u64 at = run + inc - mine;
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    if (key_at(v, j) == cut && ++at == ties)
-                        found = (uint32_t)index(v, j);
-                run += __shfl_sync(0xffffffffu, inc, 31);
-            }
+                n += R::at(q, j) > -INFINITY;
+        });
+        u64 s[1] = {__reduce_add_sync(0xffffffffu, n)};
+        cluster_sums(s, at);
+        if (s[0] > (u64)k)
+            cut = y.search(false, (u64)k, s[0], cut);
+        if (has_p) {
+            u64 z[1] = {mass_of(cut)};
+            cluster_sums(z, at);
+            z_all = z[0];
         }
-        u64 s[1] = {found == 0xffffffffu ? 0ull : (u64)found + 1};
-        cluster_sums<false>(s, sh, turn, C, rank);
-        if (s[0] > 0)
-            last_tie = (int)s[0] - 1;
     }
-    auto kept = [&](int v, int j) -> float {
-        const float l = x.at(v, j);
-        const uint32_t key = order_key(l);
-        if (key < cut || (key == cut && index(v, j) > last_tie))
-            return 0.f;
-        const float e = e_fast(l);
+    if (has_p)
+        cut = y.search(true, needed_mass(p, z_all), z_all, cut);
+    auto kept = [&](float l, int i) -> float {
+        const float e = cut.keeps(l, i) ? y.e_fast(l) : 0.f;
         return l == m || e >= mp ? e : 0.f;
     };
-    auto vector_mass = [&](int v) {
-        float f = 0.f;
+    u64 in_warp = 0;
+    x.each([&](int i0, const uint32_t(&q)[4]) {
+        float t = 0.f;
 #pragma unroll
         for (int j = 0; j < E; ++j)
-            f += kept(v, j);
-        return fixed_mass(f);
-    };
-    u64 in_lane = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-        in_lane += vector_mass(v);
-    const u64 in_warp = warp_sum64(in_lane);
+            t += kept(R::at(q, j), i0 + j);
+        in_warp += fixed_mass(t);
+    });
+    in_warp = warp_sum64(in_warp);
     u64 z;
-    const u64 before = __shfl_sync(0xffffffffu, cluster_before(lane == 0 ? in_warp : 0, z, sh, turn, C, rank), 0);
+    u64 run = cluster_before(in_warp, z, at);
     const u64 goal = goal_mass(u, z);
-    if (before <= goal && goal < before + in_warp) {
-        u64 run = before;
-        bool done = false;
+    if (run <= goal && goal < run + in_warp)
+        x.each([&](int i0, const uint32_t(&q)[4]) {
+            float t = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const u64 mine = vector_mass(v);
+            for (int j = 0; j < E; ++j)
+                t += kept(R::at(q, j), i0 + j);
+            const u64 mine = fixed_mass(t);
             u64 inc = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+                const u64 w = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o)
-                    inc += y;
+                    inc += w;
             }
-            const u64 at = run + inc - mine;
-            if (!done && at <= goal && goal < run + inc) {
+            const u64 first = run + inc - mine;
+            if (first <= goal && goal < first + mine) {
                 // this lane's vector: its elements in turn; the last kept one if their sum falls short
-                float f = 0.f;
-                const float want = __ull2float_rz(goal - at) * 0x1p-40f;
+                const float want = __ull2float_rz(goal - first) * 0x1p-40f;
+                float f = 0.f, pe = 0.f;
                 int pick = -1;
-                float pe = 0.f;
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const float e = kept(v, j);
+                    const float e = kept(R::at(q, j), i0 + j);
                     if (e > 0.f && (pick < 0 || f <= want)) {
-                        pick = index(v, j);
-                        pe = e_of(x.at(v, j));
+                        pick = i0 + j;
+                        pe = expf((R::at(q, j) - m) * inv);
                     }
                     f += e;
                 }
                 a.tokens[r] = pick;
                 if (a.probs)
                     a.probs[r] = share(pe, z);
-                done = true;
             }
             run += __shfl_sync(0xffffffffu, inc, 31);
+        });
+}
+
+__device__ __forceinline__ Place place_of(int C)
+{
+    Place at;
+    at.C = C;
+    at.rank = C > 1 ? cluster_ctarank() : 0;
+    at.lane = threadIdx.x & 31;
+    at.warp = threadIdx.x >> 5;
+    at.turn = 0;
+    return at;
+}
+
+// A row per cluster (with NV = 0 per CTA).
+template <typename T, int NV>
+__global__ void __launch_bounds__(SC_THREADS, 2)
+    k_sample(const SampleArgs a, const int C, const int per_warp, const bool defer)
+{
+    Place at = place_of(NV > 0 ? C : 1);
+    if (defer)
+        pdl_launch_dependents();
+    sample_row<T, NV>(a, at, per_warp, blockIdx.x / at.C, defer);
+}
+
+// The rows that the kernel before left.  Every CTA of a cluster reads the
+// marks of its rows before any of them ends, which takes a barrier of all.
+template <typename T, int NV>
+__global__ void __launch_bounds__(SC_THREADS, 2)
+    k_sample_pending(const SampleArgs a, const int C, const int per_warp, const int T_rows)
+{
+    Place at = place_of(C);
+    const int me = blockIdx.x / C, clusters = gridDim.x / C;
+    pdl_wait();
+    for (int r0 = 0; r0 < T_rows; r0 += 32) {
+        const int mark = r0 + at.lane < T_rows ? *(volatile int32_t *)(a.tokens + r0 + at.lane) : 0;
+        unsigned left = __ballot_sync(0xffffffffu, mark <= PENDING && (PENDING - mark) % clusters == me);
+        for (; left; left &= left - 1) {
+            sample_row<T, NV>(a, at, per_warp, r0 + __ffs(left) - 1, false);
+            __syncthreads();
         }
     }
 }
 
+enum { ROWS_ALL, ROWS_DEFER, ROWS_PENDING };
+
 template <typename T, int NV>
-cudaError_t launch_cluster(const SampleArgs &a, int T_rows, int C, int per_warp, cudaStream_t st)
+cudaError_t launch_rows(const SampleArgs &a, int T_rows, int C, int per_warp, int rows, cudaStream_t st)
 {
-    static thread_local int attr_dev = -1;  // per host thread
+    static thread_local int attr_dev[2] = {-1, -1};  // per host thread and kernel
+    const bool pending = rows == ROWS_PENDING;
     int dev = 0;
     cudaGetDevice(&dev);
-    if (attr_dev != dev) {
-        cudaError_t e = cudaFuncSetAttribute(k_sample<T, NV>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (attr_dev[pending] != dev) {
+        const void *f = reinterpret_cast<const void *>(k_sample<T, NV>);
+        if constexpr (NV > 0)
+            if (pending)
+                f = reinterpret_cast<const void *>(k_sample_pending<T, NV>);
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_sample<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)sizeof(SampleShared));
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
         if (e != cudaSuccess)
             return e;
-        attr_dev = dev;
+        attr_dev[pending] = dev;
     }
+    // (the pending rows' clusters: two CTAs an SM)
+    const int two = 2 * sm_count() / C > 0 ? 2 * sm_count() / C : 1;
+    const int clusters = pending && two < T_rows ? two : T_rows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)T_rows * C, 1, 1);
+    cfg.gridDim = dim3((unsigned)clusters * C, 1, 1);
     cfg.blockDim = dim3(SC_THREADS, 1, 1);
     cfg.dynamicSmemBytes = sizeof(SampleShared);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = C;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_sample<T, NV>, a, C, per_warp);
+    cfg.numAttrs = pending ? 2 : 1;
+    if constexpr (NV > 0)
+        if (pending)
+            return cudaLaunchKernelEx(&cfg, k_sample_pending<T, NV>, a, C, per_warp, T_rows);
+    return cudaLaunchKernelEx(&cfg, k_sample<T, NV>, a, C, per_warp, rows == ROWS_DEFER);
 }
 
-// The cluster's size and the vectors a thread holds: as few CTAs as hold a
-// row in 16 or 32 registers a thread; while the rows leave SMs idle, twice as
-// many.  Rows too long for 16 CTAs take the CTA-per-row kernel.
+template <typename T>
+cudaError_t launch_cluster(const SampleArgs &a, int T_rows, int C, int vectors, int rows, cudaStream_t st)
+{
+    const int per_warp = (vectors + C * SC_WARPS - 1) / (C * SC_WARPS), per = (per_warp + 31) / 32;
+    if (per <= 1)
+        return launch_rows<T, 1>(a, T_rows, C, per_warp, rows, st);
+    if (per <= 2)
+        return launch_rows<T, 2>(a, T_rows, C, per_warp, rows, st);
+    if (per <= 4)
+        return launch_rows<T, 4>(a, T_rows, C, per_warp, rows, st);
+    if constexpr (RowType<T>::E == 4)
+        return launch_rows<T, 8>(a, T_rows, C, per_warp, rows, st);
+    return cudaErrorInvalidValue;  // (not reached: a row is held in that many)
+}
+
+// The form.  A cluster: as few CTAs as hold a row in 16 or 32 registers a
+// thread, and while the rows leave SMs idle twice as many.  Where the
+// clusters would come in more than three rounds of two CTAs an SM, a CTA per
+// row that reads it again, and then clusters for the rows that it left (256
+// rows of 131072: 75 us in clusters, 21 us by CTAs); the CTAs alone where 16
+// do not hold a row.
 template <typename T>
 cudaError_t launch_sample(const SampleArgs &a, int T_rows, cudaStream_t st)
 {
     constexpr int E = RowType<T>::E, MOST = E == 8 ? 4 : 8;
     // (a row may begin inside a vector)
     const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && (T_rows == 1 || a.stride % E == 0);
-    const int vectors = (a.V + E - 1) / E + (aligned ? 0 : 1);
+    const int vectors = (a.V + E - 1) / E + (aligned ? 0 : 1), per_warp = (vectors + SC_WARPS - 1) / SC_WARPS;
     int C = 1;
     while (C < SC_MAX_CLUSTER && vectors > C * SC_THREADS * MOST)
         C *= 2;
-    if (vectors > C * SC_THREADS * MOST || (long long)T_rows * C > 0x7fffffffll) {
-        k_sample_simple<T><<<T_rows, SA_THREADS, 0, st>>>(a);
-        return cudaGetLastError();
+    if (vectors > C * SC_THREADS * MOST)
+        return launch_rows<T, 0>(a, T_rows, 1, per_warp, ROWS_ALL, st);
+    if (C > 1 && (long long)T_rows * C > 6ll * sm_count()) {
+        const cudaError_t e = launch_rows<T, 0>(a, T_rows, 1, per_warp, ROWS_DEFER, st);
+        return e == cudaSuccess ? launch_cluster<T>(a, T_rows, C, vectors, ROWS_PENDING, st) : e;
     }
     while (C < SC_MAX_CLUSTER && vectors > C * SC_THREADS && (long long)T_rows * C * 2 <= sm_count())
         C *= 2;
-    const int per_warp = (vectors + C * SC_WARPS - 1) / (C * SC_WARPS), per = (per_warp + 31) / 32;
-    if (per <= 1)
-        return launch_cluster<T, 1>(a, T_rows, C, per_warp, st);
-    if (per <= 2)
-        return launch_cluster<T, 2>(a, T_rows, C, per_warp, st);
-    if (per <= 4)
-        return launch_cluster<T, 4>(a, T_rows, C, per_warp, st);
-    if constexpr (MOST == 8)
-        return launch_cluster<T, 8>(a, T_rows, C, per_warp, st);
-    return cudaErrorInvalidValue;  // (not reached: per <= MOST)
+    return launch_cluster<T>(a, T_rows, C, vectors, ROWS_ALL, st);
 }
 
 }  // namespace
@@ -1292,8 +1484,7 @@ lora_status lora_sample(const void *logits_dev, int logits_type, long long row_s
                         const float *top_p_dev, const float *min_p_dev, int32_t *tokens_dev, float *probs_dev,
                         lora_stream_t stream)
 {
-    if (T < 0 || V < 1 || row_stride < V ||
-        (logits_type != LORA_TYPE_F32 && logits_type != LORA_TYPE_BF16))
+    if (T < 0 || V < 1 || row_stride < V || (logits_type != LORA_TYPE_F32 && logits_type != LORA_TYPE_BF16))
         return LORA_ERR_INVALID_ARG;
     if (V > LORA_MAX_VOCAB || T > LORA_MAX_TOKENS)
         return LORA_ERR_NOT_SUPPORTED;
