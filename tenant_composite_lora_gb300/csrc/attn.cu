@@ -350,40 +350,24 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
 
 // ---------------------------------------------------------------- combine
 
-constexpr int CB_BATCH = 4;  // pieces whose sums are on their way at a time
-
 // The pieces of one query row and head: of the prefix, then of the request's
 // own tokens, in the order of the keys.
 struct RowPieces {
     long long base[2];
     int n[2], pitch[2];
+    // g: the query head among those that share key/value head h
     __device__ __forceinline__ void find(const AttnPlanDev &p, const int4 &tok, int h, int g)
     {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int code = k ? tok.z : tok.x, r = (k ? tok.w : tok.y) + g;
-            n[k] = 0;
-            base[k] = 0;
-            pitch[k] = 0;
-            if (code < 0)
-                continue;
-            const int cls = code & 1, tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS, lead = attn_lead(cls);
-            const long long *len = p.len + cls * AL_WORDS;
-            const AttnSeg &s = p.seg[cls][(code >> 1) + r / tr];
-            if (s.ntiles == 0)
-                continue;
-            const long long a0 = s.a + (long long)h * (s.ntiles + lead) + lead, run = len[AL_RUN];
-            int c0, c1, rem;
-            if (run >> 31) {
-                c0 = (int)(a0 / run);
-                c1 = (int)((a0 + s.ntiles - 1) / run);
-            } else {
-                c0 = div_units(a0, (int)run, rem);
-                c1 = div_units(a0 + s.ntiles - 1, (int)run, rem);
-            }
-            n[k] = c1 - c0 + 1;
-            pitch[k] = p.pitch[cls];
-            base[k] = len[AL_PART] + (long long)c0 * pitch[k] + s.rows0 + (long long)h * s.nrows + r % tr;
+            const int cls = code & 1, tr = cls == AC_WIDE ? WA_ROWS : NA_ROWS;
+            AttnPieces x{0, 0, 0};
+            if (code >= 0)
+                x = p.pieces[cls][(long long)((code >> 1) + r / tr) * p.hkv + h];
+            n[k] = x.n;
+            pitch[k] = x.pitch;
+            base[k] = x.base + r % tr;
         }
     }
     __device__ __forceinline__ long long at(int i) const
@@ -392,55 +376,39 @@ struct RowPieces {
     }
 };
 
-// Joins pieces i0 .. i1 of a row relative to the maximum B: its sums (D / 32
-// elements a lane) and L.
+// A row's sums so far, on its maximum so far: D / 32 elements a lane.
 template <int D>
-__device__ __forceinline__ void join(const AttnPlanDev &p, const RowPieces &rp, int i0, int i1, float B, int lane,
-                                     float (&acc)[D / 32], float &L)
-{
-    constexpr int E = D / 32;
-    for (int i = i0; i < i1; i += CB_BATCH) {
-        float2 ml[CB_BATCH];
-        float v[CB_BATCH][E];
+struct RowSum {
+    static constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.f, acc[E] = {};
+    __device__ __forceinline__ void add(float m1, float l1, const float (&x)[E])
+    {
+        const float mx = fmaxf(m, m1), b = mx == -INFINITY ? 0.f : mx;
+        const float f0 = pow2(m - b), f1 = pow2(m1 - b);
+        m = mx;
+        l = l * f0 + l1 * f1;
 #pragma unroll
-        for (int j = 0; j < CB_BATCH; ++j)
-            if (i + j < i1) {
-                const long long pr = rp.at(i + j);
-                ml[j] = p.part_ml[pr];
-                const float *x = p.part + pr * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(x);
-                    v[j][0] = y.x;
-                    v[j][1] = y.y;
-                    v[j][2] = y.z;
-                    v[j][3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2 *>(x);
-                    v[j][0] = y.x;
-                    v[j][1] = y.y;
-                }
-            }
-#pragma unroll
-        for (int j = 0; j < CB_BATCH; ++j)
-            if (i + j < i1) {
-                const float f = pow2(ml[j].x - B);
-                L += f * ml[j].y;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    acc[e] += f * v[j][e];
-            }
+        for (int e = 0; e < E; ++e)
+            acc[e] = acc[e] * f0 + x[e] * f1;
     }
-}
+};
 
-__device__ __forceinline__ float row_max(const AttnPlanDev &p, const RowPieces &rp, int np, int lane)
+template <int D>
+__device__ __forceinline__ void load_piece(const AttnPlanDev &p, long long row, int lane, float2 &ml, float (&x)[D / 32])
 {
-    float M = -INFINITY;
-    for (int i = lane; i < np; i += 32)
-        M = fmaxf(M, p.part_ml[rp.at(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    return M;
+    ml = p.part_ml[row];
+    const float *at = p.part + row * D + lane * (D / 32);
+    if constexpr (D == 128) {
+        const float4 y = *reinterpret_cast<const float4 *>(at);
+        x[0] = y.x;
+        x[1] = y.y;
+        x[2] = y.z;
+        x[3] = y.w;
+    } else {
+        const float2 y = *reinterpret_cast<const float2 *>(at);
+        x[0] = y.x;
+        x[1] = y.y;
+    }
 }
 
 template <int D>
@@ -460,10 +428,11 @@ __device__ __forceinline__ void write_row(const AttnArgs &a, int hq_all, int t, 
 }
 
 // Many rows: a warp per (query token, key/value head) takes its query heads
-// in turn; where their pieces lie is looked up once for a row tile.
+// four at a time: their rows lie side by side.
 template <int D>
 __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const AttnArgs a)
 {
+    constexpr int H = 4;
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     pdl_wait();
@@ -473,60 +442,83 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnPlanDev p, const
     const int t = (int)(item / p.hkv), h = (int)(item % p.hkv), G = p.hq / p.hkv;
     const int4 tok = p.tok[t];
     RowPieces rp;
-    for (int g = 0; g < G; ++g) {
-        // (a token's heads may lie in two tiles; 16 divides both classes' rows)
-        if (g == 0 || (tok.y + g) % NA_ROWS == 0 || (tok.w + g) % NA_ROWS == 0) {
-            rp.find(p, tok, h, g);
-        } else {
-            ++rp.base[0];
-            ++rp.base[1];
-        }
+    for (int g = 0; g < G;) {
+        // (a token's heads may lie in two tiles, whose rows are multiples of 16 of the group's or request's)
+        const int n = min(min(H, G - g), min(NA_ROWS - (tok.y + g) % NA_ROWS, NA_ROWS - (tok.w + g) % NA_ROWS));
+        rp.find(p, tok, h, g);
         const int np = rp.n[0] + rp.n[1];
-        const float M = row_max(p, rp, np, lane);
-        float acc[D / 32] = {}, L = 0.f;
-        join<D>(p, rp, 0, np, M == -INFINITY ? 0.f : M, lane, acc, L);
-        write_row<D>(a, p.hq, t, h * G + g, acc, M, L, lane);
+        RowSum<D> s[H];
+        for (int i = 0; i < np; ++i) {
+            const long long row = rp.at(i);
+            float2 ml[H];
+            float x[H][D / 32];
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                if (j < n)
+                    load_piece<D>(p, row + j, lane, ml[j], x[j]);
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                if (j < n)
+                    s[j].add(ml[j].x, ml[j].y, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            if (j < n)
+                write_row<D>(a, p.hq, t, h * G + g + j, s[j].acc, s[j].m, s[j].l, lane);
+        g += n;
     }
 }
 
 // Few rows, whose keys are cut into many pieces: eight warps a row, an equal
-// share of its pieces each.
+// share of its pieces each, four of them on their way at a time.
 constexpr int CB_WARPS = 8;
 
 template <int D>
 __global__ void __launch_bounds__(CB_WARPS * 32) k_attn_combine_few(const AttnPlanDev p, const AttnArgs a)
 {
+    constexpr int E = D / 32, B = 4;
     __shared__ float s_acc[CB_WARPS][D];
-    __shared__ float s_l[CB_WARPS];
-    constexpr int E = D / 32;
+    __shared__ float2 s_ml[CB_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
     const int t = blockIdx.x / p.hq, hq = blockIdx.x % p.hq, G = p.hq / p.hkv;
     RowPieces rp;
     rp.find(p, p.tok[t], hq / G, hq % G);
-    const int np = rp.n[0] + rp.n[1];
-    const float M = row_max(p, rp, np, lane);
-    float acc[E] = {}, L = 0.f;
-    join<D>(p, rp, warp * np / CB_WARPS, (warp + 1) * np / CB_WARPS, M == -INFINITY ? 0.f : M, lane, acc, L);
+    const int np = rp.n[0] + rp.n[1], i0 = warp * np / CB_WARPS, i1 = (warp + 1) * np / CB_WARPS;
+    RowSum<D> s;
+    for (int i = i0; i < i1; i += B) {
+        float2 ml[B];
+        float x[B][E];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (i + j < i1)
+                load_piece<D>(p, rp.at(i + j), lane, ml[j], x[j]);
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (i + j < i1)
+                s.add(ml[j].x, ml[j].y, x[j]);
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        s_acc[warp][lane * E + e] = acc[e];
+        s_acc[warp][lane * E + e] = s.acc[e];
     if (lane == 0)
-        s_l[warp] = L;
+        s_ml[warp] = make_float2(s.m, s.l);
     __syncthreads();
     if (warp > 0)
         return;
+#pragma unroll
     for (int v = 1; v < CB_WARPS; ++v) {
-        L += s_l[v];
+        float x[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            acc[e] += s_acc[v][lane * E + e];
+            x[e] = s_acc[v][lane * E + e];
+        s.add(s_ml[v].x, s_ml[v].y, x);
     }
-    write_row<D>(a, p.hq, t, hq, acc, M, L, lane);
+    write_row<D>(a, p.hq, t, hq, s.acc, s.m, s.l, lane);
 }
 
-constexpr int CB_FEW = 1216;  // rows: eight warps an SM of 152 at one warp a row
+constexpr int CB_FEW = 4096;  // rows that take eight warps each
 
 template <int D>
 cudaError_t run_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)

@@ -39,10 +39,10 @@ constexpr int NA_KEYS = 16;
 constexpr int NA_WARPS = 4;        // of a CTA
 constexpr int NA_CTAS_PER_SM = 3;
 constexpr int NA_LEAD = 3;         // units
-constexpr int NA_MIN_RUN = 4;
+constexpr int NA_MIN_RUN = 2;
 constexpr int WA_ROWS = 256;
 constexpr int WA_KEYS = 128;
-constexpr int WA_LEAD = 2;
+constexpr int WA_LEAD = 5;
 constexpr int WA_MIN_RUN = 3;
 enum { AC_NARROW = 0, AC_WIDE = 1 };  // class of a segment
 
@@ -55,6 +55,13 @@ struct AttnSeg {
     int ntiles;       // of each head
     int src;          // request, or ~group
     int lim;          // token t sees the first min(nkeys, max(0, t + lim)) keys
+};
+
+// Where a segment's pieces of one head lie: n of them, the first one's first
+// partial row (of the segment's row 0), a class's pitch apart.
+struct AttnPieces {
+    long long base;
+    int n, pitch;
 };
 
 // Header words of a plan (device int32).
@@ -76,6 +83,7 @@ struct AttnPlanDev {
     int32_t *s_pages;  // [max_requests][max_spages]
     int32_t *p_pages;  // [max_groups][max_ppages]
     AttnSeg *seg[2];      // [max_segs] per class
+    AttnPieces *pieces[2];  // [max_segs][hkv]
     int32_t *run_seg[2];  // [workers] segment in which each worker's run begins
     float *part;       // [part_rows][d]
     float2 *part_ml;   // [part_rows] running maximum (in units of log 2) and sum

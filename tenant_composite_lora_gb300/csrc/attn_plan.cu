@@ -181,6 +181,19 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
                 p.len[c * AL_WORDS + AL_PART] =
                     c == AC_NARROW ? 0 : (long long)p.workers[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
             }
+            const long long part0 =
+                c == AC_NARROW ? 0 : (long long)p.workers[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
+            for (long long x = tid; x < segs[c] * p.hkv; x += AP_THREADS) {
+                const AttnSeg &g = p.seg[c][x / p.hkv];
+                const int h = (int)(x % p.hkv), lead = attn_lead(c);
+                AttnPieces k{0, 0, p.pitch[c]};
+                if (g.ntiles > 0) {
+                    const long long u = g.a + (long long)h * (g.ntiles + lead) + lead, w = u / run;
+                    k.n = (int)((u + g.ntiles - 1) / run - w) + 1;
+                    k.base = part0 + w * p.pitch[c] + g.rows0 + (long long)h * g.nrows;
+                }
+                p.pieces[c][x] = k;
+            }
             for (int x = tid; x < p.workers[c]; x += AP_THREADS) {
                 const long long at = x * run;
                 int lo = 0, hi = (int)segs[c];  // last segment starting at or before `at`: the one that holds it
@@ -261,7 +274,7 @@ void free_plan(lora_attn_plan *p)
         return;
     AttnPlanDev &d = p->dev;
     void *all[] = {d.hdr,    d.len,    d.sseg,       d.pseg,       d.tok,  d.s_pages, d.p_pages,
-                   d.seg[0], d.seg[1], d.run_seg[0], d.run_seg[1], d.part, d.part_ml};
+                   d.seg[0], d.seg[1], d.pieces[0], d.pieces[1], d.run_seg[0], d.run_seg[1], d.part, d.part_ml};
     for (void *x : all)
         if (x)
             cudaFree(x);
@@ -336,6 +349,7 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     if (e == cudaSuccess) e = plan_alloc(&d.p_pages, (size_t)max_groups * max_prefix_pages);
     for (int c = 0; c < 2; ++c) {
         if (e == cudaSuccess) e = plan_alloc(&d.seg[c], (size_t)segs);
+        if (e == cudaSuccess) e = plan_alloc(&d.pieces[c], (size_t)segs * n_kv_heads);
         if (e == cudaSuccess) e = plan_alloc(&d.run_seg[c], (size_t)d.workers[c]);
     }
     if (e == cudaSuccess) e = plan_alloc(&d.part, (size_t)part_rows * head_dim);
