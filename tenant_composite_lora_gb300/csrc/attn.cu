@@ -16,7 +16,8 @@
 //    a store.  Bound by the cache's bytes.
 //  * k_attn_wide (attn_wide.cu): tiles of 256 rows and 128 keys on the tensor
 //    memory's matrix instructions, for prefixes of many requests and for
-//    prefill chunks.
+//    prefill chunks.  In a batch with both it runs beside the narrow kernel,
+//    on SMs of its own (attn_unit_ns).
 //  * k_attn_combine: joins each row's pieces (the key axis is cut over the
 //    SMs, see attn.h) and rounds once.
 #include <cstring>
@@ -79,9 +80,9 @@ __device__ __forceinline__ uint32_t na_chunk(int key, int c)
 }
 
 template <int D>
-__global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
+__global__ void __launch_bounds__(NA_THREADS, 1)
     k_attn_narrow(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const AttnPlanDev p, const AttnArgs a, const bool after_wide)
+                  const AttnPlanDev p, const AttnArgs a)
 {
     typedef NaShape<D> S;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -101,17 +102,16 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
         fence_mbar_init();
     }
     __syncwarp();
-    // the plan, q and the cache; the partial rows' last reader.  After the wide kernel all of it is there: each of
-    // its CTAs let this kernel start only once it had waited itself.  The two work side by side, and this one
-    // ends after it, so that the combine kernel's wait covers both.
-    if (!after_wide)
-        pdl_wait();
+    pdl_wait();  // the plan, q and the cache; the partial rows' last reader
     pdl_launch_dependents();
     int32_t *status = p.hdr + AH_STATUS;
     const int G = p.hq / p.hkv;
     const int r0 = lane >> 2, r1 = r0 + 8, c2 = (lane & 3) * 2;
     const uint32_t ring_u = smem_u32(ring);
-    const int worker = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
+    const int ctas = (int)p.len[AC_NARROW * AL_WORDS + AL_CTAS];
+    if ((int)blockIdx.x >= ctas)
+        return;
+    const int worker = warp * ctas + blockIdx.x;  // neighbouring runs on different SMs
 
     // ---- the loads: the walk over the run's tiles, a stage ahead of the products
     PieceWalk<AC_NARROW> w(p, worker);
@@ -344,8 +344,6 @@ __global__ void __launch_bounds__(NA_THREADS, NA_CTAS_PER_SM)
     for (; it < loaded && !ok; ++it)
         if (!mbar_wait_now(&full[it % S::STAGES], (it / S::STAGES) & 1, status))
             break;
-    if (after_wide)
-        pdl_wait();
 }
 
 // ---------------------------------------------------------------- combine
@@ -541,15 +539,15 @@ cudaError_t run_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cach
     const bool wide = (long long)a.TQ * G > NA_ROWS;
     const bool narrow = G <= NA_ROWS && (!wide || a.B > 1);
     cudaError_t e = cudaSuccess;
-    if (wide)
-        e = launch_attn_wide(p, a, cache, st);
-    if (e == cudaSuccess && narrow) {
+    if (narrow) {
         CUtensorMap mk, mv;
         std::memcpy(&mk, cache.map_k[AC_NARROW], sizeof(mk));
         std::memcpy(&mv, cache.map_v[AC_NARROW], sizeof(mv));
         e = launch_pdl(k_attn_narrow<D>, dim3(p.workers[AC_NARROW] / NA_WARPS), NA_THREADS, NaShape<D>::SMEM, st, mk,
-                       mv, p, a, wide);
+                       mv, p, a);
     }
+    if (e == cudaSuccess && wide)
+        e = launch_attn_wide(p, a, cache, narrow, st);
     if (e != cudaSuccess)
         return e;
     const long long rows = (long long)a.TQ * p.hq;

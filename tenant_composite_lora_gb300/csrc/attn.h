@@ -36,8 +36,7 @@ constexpr int ATTN_BOX_MAX = 64;
 // least nrows from a piece to the next one.
 constexpr int NA_ROWS = 16;
 constexpr int NA_KEYS = 16;
-constexpr int NA_WARPS = 4;        // of a CTA
-constexpr int NA_CTAS_PER_SM = 3;
+constexpr int NA_WARPS = 12;       // of a CTA, one to an SM
 constexpr int NA_LEAD = 3;         // units
 constexpr int NA_MIN_RUN = 2;
 constexpr int WA_ROWS = 256;
@@ -65,9 +64,18 @@ struct AttnPieces {
 };
 
 // Header words of a plan (device int32).
-enum { AH_STATUS = 0, AH_NREQ = 1, AH_NGRP = 2, AH_WORDS = 16 };
-// Per class: its sequence's units, each worker's run, its first partial row (device int64).
-enum { AL_UNITS = 0, AL_RUN = 1, AL_PART = 2, AL_WORDS = 4 };
+enum { AH_STATUS = 0, AH_WORDS = 16 };
+// Per class: its sequence's units, each worker's run, its first partial row, the CTAs that work on it (device int64).
+enum { AL_UNITS = 0, AL_RUN = 1, AL_PART = 2, AL_CTAS = 3, AL_WORDS = 4 };
+// What a unit costs an SM, in nanoseconds, while both classes are at work: a batch with both shares the SMs out by
+// it, and the two kernels run side by side -- the narrow one waits for the cache's bytes, the wide one for its
+// products.  Measured, 32 requests behind 4099 keys, 256 behind 32768, 64 in 16 groups (head_dim 128) and 24
+// with 8 tokens each (head_dim 64): 24, 161, 78 and 31 us; each kernel on all SMs, one after the other:
+// 29, 162, 92 and 35 us; 30 % more or less for the narrow one: up to 15 % more.
+__host__ __device__ constexpr int attn_unit_ns(int cls, int d)
+{
+    return cls == AC_WIDE ? (d == 64 ? 1100 : 1950) : (d == 64 ? 52 : 105);
+}
 
 __host__ __device__ constexpr int attn_lead(int cls) { return cls == AC_WIDE ? WA_LEAD : NA_LEAD; }
 
@@ -110,7 +118,8 @@ struct AttnArgs {
     bool q_map;        // the wide kernel's queries come by TMA
 };
 cudaError_t launch_attn(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
-cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st);
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, bool after_narrow,
+                             cudaStream_t st);
 
 }  // namespace tcl
 

@@ -101,12 +101,8 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
         bad = __syncthreads_or(bad);
         badg = __syncthreads_or(badg);
         const int B = bad ? 0 : s.B, NG = bad || badg ? 0 : s.NG;
-        if (tid == 0) {
-            if (bad || badg)
-                atomicOr(status, LORA_DEV_BAD_LENGTH);
-            p.hdr[AH_NREQ] = B;
-            p.hdr[AH_NGRP] = NG;
-        }
+        if (tid == 0 && (bad || badg))
+            atomicOr(status, LORA_DEV_BAD_LENGTH);
         // the segments: groups, then requests
         const int G = p.hq / p.hkv;
         long long segs[2] = {0, 0}, units_of[2] = {0, 0}, rows[2] = {0, 0};
@@ -171,13 +167,23 @@ __global__ void __launch_bounds__(AP_THREADS) k_attn_plan(const AttnPlanDev p, c
             }
         }
         __syncthreads();  // the segments are written (by this block)
+        const int sms = p.workers[AC_WIDE];
+        int ctas[2] = {sms, sms};
+        if (units_of[AC_NARROW] > 0 && units_of[AC_WIDE] > 0) {
+            const float n = (float)units_of[AC_NARROW] * attn_unit_ns(AC_NARROW, p.d);
+            const float w = (float)units_of[AC_WIDE] * attn_unit_ns(AC_WIDE, p.d);
+            ctas[AC_NARROW] = min(sms - 1, max(1, (int)(sms * (n / (n + w)) + 0.5f)));
+            ctas[AC_WIDE] = max(1, sms - ctas[AC_NARROW]);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int least = c == AC_WIDE ? WA_MIN_RUN : NA_MIN_RUN;
-            const long long run = max((long long)least, (units_of[c] + p.workers[c] - 1) / p.workers[c]);
+            const int workers = ctas[c] * (c == AC_WIDE ? 1 : NA_WARPS);
+            const long long run = max((long long)least, (units_of[c] + workers - 1) / workers);
             if (tid == 0) {
                 p.len[c * AL_WORDS + AL_UNITS] = units_of[c];
                 p.len[c * AL_WORDS + AL_RUN] = run;
+                p.len[c * AL_WORDS + AL_CTAS] = ctas[c];
                 p.len[c * AL_WORDS + AL_PART] =
                     c == AC_NARROW ? 0 : (long long)p.workers[AC_NARROW] * p.pitch[AC_NARROW] + rows[AC_NARROW];
             }
@@ -324,7 +330,7 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     d.d = head_dim;
     d.page = page_size;
     d.page_log2 = __builtin_ctz((unsigned)page_size);
-    d.workers[AC_NARROW] = NA_WARPS * NA_CTAS_PER_SM * sm_count();
+    d.workers[AC_NARROW] = NA_WARPS * sm_count();
     d.workers[AC_WIDE] = sm_count();
     // a row tile of every group and request and one per full tile of rows;
     // a query row has partial rows for the prefix and the request's own
@@ -341,7 +347,7 @@ lora_status lora_attn_plan_create(int max_requests, int max_groups, int max_quer
     }
     d.max_segs = (int)segs;
     cudaError_t e = plan_alloc(&d.hdr, AH_WORDS);
-    if (e == cudaSuccess) e = plan_alloc(&d.len, AL_WORDS);
+    if (e == cudaSuccess) e = plan_alloc(&d.len, 2 * AL_WORDS);
     if (e == cudaSuccess) e = plan_alloc(&d.sseg, (size_t)max_requests);
     if (e == cudaSuccess) e = plan_alloc(&d.pseg, (size_t)max_groups);
     if (e == cudaSuccess) e = plan_alloc(&d.tok, (size_t)max_queries);

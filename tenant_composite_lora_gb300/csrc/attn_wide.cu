@@ -507,7 +507,7 @@ template <int D>
 __global__ void __launch_bounds__(WA_THREADS, 1)
     k_attn_wide(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ CUtensorMap mq, const AttnPlanDev p, const AttnArgs a,
-                const __nv_bfloat16 *vcache)
+                const __nv_bfloat16 *vcache, const bool after_narrow)
 {
     typedef WaShape<D> S;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -515,6 +515,13 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
                                                             ~static_cast<uintptr_t>(1023));
     __shared__ WaBars bar;
     const int tid = threadIdx.x, warp = tid >> 5;
+    // The plan, q and the cache; the partial rows' last reader.  After the narrow kernel all of it is there: its CTAs
+    // let this kernel start only once they had waited themselves.  The two work side by side, and this one ends
+    // after it, so that the combine kernel's wait covers both.
+    if (after_narrow && (int)blockIdx.x >= (int)p.len[AC_WIDE * AL_WORDS + AL_CTAS]) {
+        pdl_wait();
+        return;  // (its SM is the narrow kernel's)
+    }
     if (tid == 0) {
         for (int s = 0; s < S::SLOTS; ++s) {
             mbar_init(&bar.full[s], 1);
@@ -535,7 +542,8 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    pdl_wait();  // the plan, q and the cache; the partial rows' last reader
+    if (!after_narrow)
+        pdl_wait();
     pdl_launch_dependents();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WA_REGS_ROWS));
@@ -555,10 +563,13 @@ __global__ void __launch_bounds__(WA_THREADS, 1)
     tc_fence_after();
     if (warp == 9)
         tmem_dealloc(bar.taddr, 512);
+    if (after_narrow)
+        pdl_wait();
 }
 
 template <int D>
-cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)
+cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, bool after_narrow,
+                     cudaStream_t st)
 {
     static thread_local int attr_dev = -1;  // per host thread
     int dev = 0;
@@ -582,14 +593,15 @@ cudaError_t run_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cach
                encode_q_heads(&mq, a.q, p.d, p.hq, a.TQ, a.q_stride, G, WA_HALF / G) == cudaSuccess;
     const __nv_bfloat16 *v = cache.v;
     return launch_pdl(k_attn_wide<D>, dim3(p.workers[AC_WIDE]), WA_THREADS, WaShape<D>::SMEM, st, mk, mv, mq, p,
-                      aw, v);
+                      aw, v, after_narrow);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, cudaStream_t st)
+cudaError_t launch_attn_wide(const AttnPlanDev &p, const AttnArgs &a, const lora_kv_cache &cache, bool after_narrow,
+                             cudaStream_t st)
 {
-    return p.d == 64 ? run_wide<64>(p, a, cache, st) : run_wide<128>(p, a, cache, st);
+    return p.d == 64 ? run_wide<64>(p, a, cache, after_narrow, st) : run_wide<128>(p, a, cache, after_narrow, st);
 }
 
 }  // namespace tcl
