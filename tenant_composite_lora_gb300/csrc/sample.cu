@@ -11,16 +11,22 @@
 //     from the threads' own maxima.
 //  2. A bound below which no kept token lies: that one, min-p's from its
 //     definition, top-p's from the mass above a few trial bounds.
-//  3. The few candidates above it go to one CTA, which cuts and picks.
-//  4. Rows with too many of them (nearly flat ones): the cut is searched
-//     for, three thresholds a pass, until so few tokens are left around it
-//     that one CTA can take those; then the kept masses in index order.
+//  3. The few candidates above it go to one CTA, which cuts and picks: up to
+//     512 by comparing each with each, up to 2048 by bisection.
+//  4. Rows with too many of them (nearly flat ones): a top-p's cut from the
+//     masses by size, in 4096 bins of shared memory, which leave a few
+//     hundred tokens about it; any other by search, three thresholds a pass,
+//     until one CTA can take those about the cut; then the kept masses in
+//     index order.
 //
 // Two forms of one kernel.  With few rows a cluster of CTAs holds a row in
 // registers (one read of the logits); with many, or with rows too long for
 // that, a CTA a row reads it again from the L2 in each pass, so that all
-// rows are under way at once.  Bound by the logits' bytes and by the latency
-// of the steps, some ten barriers a row.
+// rows are under way at once.  Bound by the latency of the steps, some ten
+// barriers a row (one row of 131072 in 32 bits: 12 us, 0.08 us by its bytes;
+// 64 rows of 32768 with settings of their own: 29 us, 39 us with the search
+// alone), and with many rows by the instructions of the passes (256 rows of
+// 131001: 118 us, 9.9 us by their bytes).
 #include <type_traits>
 
 #include "internal.h"
@@ -33,7 +39,7 @@ namespace {
 constexpr int SC_THREADS = 512, SC_WARPS = SC_THREADS / 32;
 constexpr int SC_LIST = 2048;   // candidates that one CTA takes
 constexpr int SC_SLOTS = 4096;  // places for them, an equal share for each CTA of the cluster
-constexpr int SC_FEW = 256;     // of these, those that are compared each with each
+constexpr int SC_FEW = SC_THREADS;  // of these, those that are compared each with each
 constexpr int SC_MAX_CLUSTER = 16;
 static_assert(SC_MAX_CLUSTER <= SC_WARPS, "a warp moves a CTA's candidates");
 
@@ -117,9 +123,22 @@ __device__ __forceinline__ void st_cluster(V *local, uint32_t rank, V x)
     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t *local, uint32_t rank)
+{
+    uint32_t a, x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+
+constexpr int SH_BINS = 4096, SH_OCTAVE = 128;  // bins of the masses by size, per octave
+
 struct SampleShared {
     // rank 0: the candidates (order key, index), SC_SLOTS / C places for each CTA's; then all in a row, by index
-    alignas(16) u64 slots[SC_SLOTS];
+    union {
+        alignas(16) u64 slots[SC_SLOTS];
+        uint32_t bins[SH_BINS];
+    };
     alignas(16) u64 list[SC_LIST];
     alignas(16) u64 mass[SC_FEW];  // theirs, where they are few
     uint32_t warp32[SC_WARPS];
@@ -128,6 +147,7 @@ struct SampleShared {
     u64 x64[2][8][SC_MAX_CLUSTER];
     u64 part[2][8][SC_WARPS];
     u64 cut;
+    u64 edge[2];  // bins about a cut
 };
 // (dynamic shared memory, whose address space functions that are not inlined know too)
 __device__ __forceinline__ SampleShared &sample_shared()
@@ -480,6 +500,41 @@ __device__ __noinline__ void pick_of_many(const SampleArgs &a, const PickArgs g)
 
 // The tokens left around a cut, as the list: the cut itself (order key,
 // index) to sh.cut.  `need`: the mass or count that they have to reach.
+// At most SC_FEW: each one's mass from a comparison with every other one.
+__device__ __noinline__ void cut_of_few(int n, bool by_mass, u64 need, float m, float inv, int turn)
+{
+    SampleShared &sh = sample_shared();
+    const int i = threadIdx.x, np = (n + 3) / 4 * 4;
+    const u64 x = i < n ? sh.list[i] : 0, place = (x & 0xffffffff00000000ull) | (uint32_t)~(uint32_t)x;
+    u64 w = 0;
+    if (i < n)
+        w = by_mass ? fixed_mass(expf((key_logit((uint32_t)(x >> 32)) - m) * inv)) : 1;
+    u64 all[1] = {w};
+    block_sums(all, turn);
+    if (all[0] == 0)  // no token here has a mass: the last one
+        w = i < n;
+    need = all[0] ? min(need, all[0]) : (u64)n;
+    if (i < np) {
+        sh.mass[i] = w;
+        sh.slots[i] = i < n ? place : 0;
+    }
+    __syncthreads();
+    if (i < n) {
+        u64 before = 0;
+        for (int j = 0; j < np; j += 4) {
+            const ulonglong2 l0 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j]);
+            const ulonglong2 l1 = *reinterpret_cast<const ulonglong2 *>(&sh.slots[j + 2]);
+            const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(&sh.mass[j]);
+            const ulonglong2 m1 = *reinterpret_cast<const ulonglong2 *>(&sh.mass[j + 2]);
+            before += (l0.x > place ? m0.x : 0) + (l0.y > place ? m0.y : 0) + (l1.x > place ? m1.x : 0) +
+                      (l1.y > place ? m1.y : 0);
+        }
+        if (before < need && need <= before + w)
+            sh.cut = x;
+    }
+    __syncthreads();
+}
+
 __device__ __noinline__ void cut_of_list(int n, bool by_mass, u64 need, float m, float inv, int turn)
 {
     SampleShared &sh = sample_shared();
@@ -678,7 +733,7 @@ struct Sampler {
     __device__ __forceinline__ bool gather(float least, int &n, P keep)
     {
         SampleShared &sh = sample_shared();
-        const int set = at.turn++ & 1, room = SC_SLOTS / at.C;
+        const int set = at.turn++ & 1, room = min(SC_SLOTS / at.C, SC_LIST);
         uint32_t count = 0;
         auto some = [&](const uint32_t (&q)[4]) { return Row<T, NV>::vector_max(q) >= least; };
         auto append = [&](int i0, const uint32_t (&q)[4], uint32_t &to, uint32_t end, u64 *slots) {
@@ -704,13 +759,8 @@ struct Sampler {
                 for (int j = 0; j < E; ++j) {
                     const float l = R::at(q, j);
                     if (keep(l, i0 + j)) {
-                        if (p < end) {
-                            const u64 y = (u64)order_key(l + 0.f) << 32 | (uint32_t)(i0 + j);
-                            if (at.C > 1)
-                                st_cluster(&slots[p], 0u, y);
-                            else
-                                slots[p] = y;
-                        }
+                        if (p < end)
+                            slots[p] = (u64)order_key(l + 0.f) << 32 | (uint32_t)(i0 + j);
                         ++p;
                     }
                 }
@@ -733,10 +783,13 @@ struct Sampler {
             if (k) {
                 uint32_t to = __reduce_add_sync(0xffffffffu, at.lane < at.warp ? w : 0u);
                 x.each([&](int i0, const uint32_t(&q)[4]) {
-                    append(i0, q, to, (uint32_t)room, sh.slots + at.rank * room);
+                    append(i0, q, to, (uint32_t)room, sh.list);
                 });
             }
             __syncthreads();
+            // (from here in whole lines: single ones cost rank 0 far more)
+            for (uint32_t i = threadIdx.x; i < min(count, (uint32_t)room); i += SC_THREADS)
+                st_cluster(&sh.slots[at.rank * room + i], 0u, sh.list[i]);
             if (threadIdx.x < at.C)
                 st_cluster(&sh.x64[set][0][at.rank], threadIdx.x, (u64)count);
             at.barrier();
@@ -777,96 +830,138 @@ struct Sampler {
         return true;
     }
 
-    // Thresholds about the cut, from a sample of the row (with NV = 0, where
-    // a pass over all of it is dear): 16 elements a thread, evenly spread.
-    // Narrows until 1.5 standard errors of the sample's share lie between.
-    __device__ __forceinline__ void guess(bool by_mass, float part, const Cut in, float (&t)[3])
+    // Rank 0's list holds the n tokens left around the cut: the cut, in every thread.
+    __device__ __forceinline__ Cut cut_of(int n, bool by_mass, u64 need)
     {
-        constexpr int SV = 16 / E;
-        uint32_t q[SV][4];
-        const int apart = max(1, (x.per_warp + 31) / 32 / SV);
+        SampleShared &sh = sample_shared();
+        const int set = at.turn++ & 1;
+        if (at.rank == 0) {
+            __syncthreads();
+            if (n <= SC_FEW)
+                cut_of_few(n, by_mass, need, m, inv, at.turn);
+            else
+                cut_of_list(n, by_mass, need, m, inv, at.turn);
+            if (threadIdx.x < at.C)
+                st_cluster(&sh.x64[set][1][0], threadIdx.x, sh.cut);
+        }
+        at.barrier();
+        const u64 cut = sh.x64[set][1][0];
+        at.turn += 64;  // (rank 0 went on from here in the CTA's own exchanges)
+        at.barrier();
+        return Cut{key_logit((uint32_t)(cut >> 32)), (int)(uint32_t)cut};
+    }
+
+    // The cut that `need` of the mass reaches, from the masses by size: bins of 1/128 of an octave, whose integer
+    // sums are good to 2^-(bits - 1) of each, say between which logits it lies.  If few tokens do, and the exact
+    // masses above the two agree, one CTA takes those.
+    __device__ __noinline__ bool cut_by_bins(u64 need, Cut &cut)
+    {
+        SampleShared &sh = sample_shared();
+        const int tid = threadIdx.x, bits = min(16, __clz(x.V));  // (V sums of less than 2^bits)
+        __syncthreads();  // the slots' last readers
+        for (int i = tid; i < SH_BINS / 4; i += SC_THREADS)
+            reinterpret_cast<uint4 *>(sh.bins)[i] = make_uint4(0, 0, 0, 0);
+        if (tid < 2)
+            sh.edge[tid] = SH_BINS;
+        __syncthreads();
+        x.each([&](int, const uint32_t(&q)[4]) {
 #pragma unroll
-        for (int i = 0; i < SV; ++i)
-            x.read(i * apart, q[i]);
-        u64 none[1] = {};
-        cluster_sums(none, at);  // (its barrier: the sums below use the same words)
-        float a = 0.f, b = 0.f;
-        u64 all = 0, f_a = 0, f_b = 0;
-        for (int step = 0; step < 10; ++step) {
-            if (step == 1) {  // from the least token on; where that is -inf or far off, what has a mass
-                a = m - 30.f / c2;
-                if (!(a > -INFINITY))
-                    return;
-                b = m;
+            for (int j = 0; j < E; ++j) {
+                const uint32_t b = min(__float_as_uint(e_fast(R::at(q, j))), 0x3f7fffffu);
+                const uint32_t bin = (0x3f7fffffu - b) >> 16;
+                if (bin < SH_BINS)
+                    atomicAdd(&sh.bins[bin], ((b & 0x7fffffu) + 0x800000u) >> (24 - bits));
             }
-            const float w = (b - a) * 0.25f;
-            const float c[3] = {step ? a + w : -INFINITY, a + 2.f * w, a + 3.f * w};
-            u64 s[3] = {};
+        });
+        at.barrier();
+        // each CTA adds up its share of the bins
+        constexpr int PER = SH_BINS / SC_THREADS;
+        const int mine = SH_BINS / at.C, per = (mine + SC_THREADS - 1) / SC_THREADS;
+        u64 w[PER], sum = 0;
 #pragma unroll
-            for (int i = 0; i < SV; ++i) {
-                float f0 = 0.f, f1 = 0.f, f2 = 0.f;
+        for (int i = 0; i < PER; ++i) {
+            const int at_bin = tid * per + i, bin = at.rank * mine + at_bin;
+            u64 h = 0;
+            if (i < per && at_bin < mine)
+                for (int r = 0; r < at.C; ++r)
+                    h += ld_cluster(&sh.bins[bin], r);
+            w[i] = h << (40 - bits) >> (bin / SH_OCTAVE);
+            sum += w[i];
+        }
+        u64 inc = sum, all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (at.lane >= o)
+                inc += y;
+        }
+        u64 run = cluster_before(__shfl_sync(0xffffffffu, inc, 31), all, at) + inc - sum;
+        const u64 margin = need >> (bits - 3);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const u64 goal = k ? need + margin : need - margin;
+                if (run < goal && goal <= run + w[i])
+                    for (int r = 0; r < at.C; ++r)
+                        st_cluster(&sh.edge[k], (uint32_t)r, (u64)(at.rank * mine + tid * per + i));
+            }
+            run += w[i];
+        }
+        at.barrier();
+        const uint32_t b0 = (uint32_t)sh.edge[0], b1 = (uint32_t)sh.edge[1];
+        const float hi = b0 == 0 ? INFINITY : m + log2f(__uint_as_float(0x3f7fffffu - (b0 << 16))) / c2;
+        const float lo =
+            b1 == SH_BINS ? -INFINITY : m + log2f(__uint_as_float(0x3f7fffffu - ((b1 + 1) << 16))) / c2;
+        u64 s[2] = {};
+        float t0 = 0.f, t1 = 0.f;
+        x.each(
+            [&](int, const uint32_t(&q)[4]) {
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const float l = R::at(q[i], j);
-                    const float e = in.keeps(l, x.index(i * apart) + j) ? by_mass ? e_fast(l) : 1.f : 0.f;
-                    f0 += l >= c[0] ? e : 0.f;
-                    f1 += l >= c[1] ? e : 0.f;
-                    f2 += l >= c[2] ? e : 0.f;
+                    const float l = R::at(q, j), e = e_fast(l);
+                    t0 += l >= hi ? e : 0.f;
+                    t1 += l >= lo ? e : 0.f;
                 }
-                s[0] += fixed_mass(f0);
-                s[1] += fixed_mass(f1);
-                s[2] += fixed_mass(f2);
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                s[i] = warp_sum64(s[i]);
-            cluster_sums(s, at);
-            if (step == 0) {
-                all = f_a = s[0];
-                f_b = 0;
-                continue;
-            }
-            const u64 want = (u64)(__ull2float_rn(all) * part);
-            const int up = s[2] >= want ? 3 : s[1] >= want ? 2 : s[0] >= want ? 1 : 0;
-            f_a = up ? s[up - 1] : f_a;
-            f_b = up < 3 ? s[up] : f_b;
-            b = up < 3 ? c[up] : b;
-            a = up ? c[up - 1] : a;
-            if (f_a - f_b <= (all >> 7))
-                break;
-        }
-        t[0] = a - (b - a);
-        t[1] = 0.5f * (a + b);
-        t[2] = b + (b - a);
+            },
+            [&] {
+                s[0] += fixed_mass(t0);
+                s[1] += fixed_mass(t1);
+                t0 = t1 = 0.f;
+            });
+        s[0] = warp_sum64(s[0]);
+        s[1] = warp_sum64(s[1]);
+        cluster_sums(s, at);
+        int n;
+        if (s[0] >= need || s[1] < need ||
+            !gather(lo, n, [&](float l, int) { return l >= lo && l < hi && l > -INFINITY; }) || n == 0)
+            return false;
+        cut = cut_of(n, true, need - s[0]);
+        return true;
     }
 
     // The cut that `need` of the mass (or of the tokens) kept by `in`
-    // reaches; all of them, `total`, reach it.
-    __device__ __noinline__ Cut search(bool by_mass, u64 need, u64 total, const Cut in)
+    // reaches; all of them reach it.
+    __device__ __noinline__ Cut search(bool by_mass, u64 need, const Cut in)
     {
         SampleShared &sh = sample_shared();
-        // (in registers a pass is cheap: some multiples of the temperature below the maximum)
-        float first[3] = {m - 16.f / c2, m - 8.f / c2, m - 4.f / c2};
-        if (NV == 0)
-            guess(by_mass, __ull2float_rn(need) / __ull2float_rn(total), in, first);
+        if (by_mass && in.l == -INFINITY) {
+            Cut cut;
+            if (cut_by_bins(need, cut))
+                return cut;
+        }
         // what is at or above a reaches it, what is at or above b does not
         uint32_t a = max(order_key(in.l), KEY_LOWEST + 1), b = order_key(m) + 1;
         u64 over = 0, n_over = 0, n_a = ~0ull;  // at or above b: mass or count, and count; count at or above a
         for (int step = 0; b - a > 1; ++step) {
-            // three thresholds between: the guess; where it missed, close by; then by turns evenly in the logits, which halves the tokens of a smooth
-            // distribution soonest, and evenly in the keys, which ends
+            // three thresholds between: evenly in the logits, which quarters the tokens of a smooth distribution
+            // soonest, and from the seventh on by turns evenly in the keys, which ends
             uint32_t t[3];
-            const float la = key_logit(a), lb = key_logit(b - 1);
+            const float la = step == 0 ? fmaxf(key_logit(a), m - 32.f / c2) : key_logit(a), lb = key_logit(b - 1);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 t[i] = a + (uint32_t)(((u64)(b - a) * (i + 1)) >> 2);
-                if (step == 0 && first[i] > -INFINITY)
-                    t[i] = order_key(first[i] + 0.f);
-                else if (NV == 0 && step == 1 && a == order_key(first[2] + 0.f))
-                    t[i] = order_key(first[2] + (first[2] - first[1]) * (i == 0 ? 1.f : i == 1 ? 3.f : 8.f) + 0.f);
-                else if (NV == 0 && step == 1 && b == order_key(first[0] + 0.f))
-                    t[i] = order_key(first[0] - (first[2] - first[1]) * (i == 0 ? 8.f : i == 1 ? 3.f : 1.f) + 0.f);
-                else if (!(step & 1) && la > -INFINITY && lb < INFINITY)
+                if ((step < 6 || !(step & 1)) && la > -INFINITY && lb < INFINITY)
                     t[i] = order_key(la + (lb - la) * (0.25f * (i + 1)) + 0.f);
                 t[i] = min(max(t[i], a + 1), b - 1);
             }
@@ -938,20 +1033,8 @@ struct Sampler {
                 const bool fits = gather(fa, n_list, [&](float l, int i) {
                     return l >= fa && !(l >= fb) && in.keeps(l, i);
                 });
-                if (fits && n_list > 0) {
-                    const int set = at.turn++ & 1;
-                    if (at.rank == 0) {
-                        __syncthreads();
-                        cut_of_list(n_list, by_mass, need - over, m, inv, at.turn);
-                        if (threadIdx.x < at.C)
-                            st_cluster(&sh.x64[set][1][0], threadIdx.x, sh.cut);
-                    }
-                    at.barrier();
-                    const u64 cut = sh.x64[set][1][0];
-                    at.turn += 64;  // (rank 0 went on from here in the CTA's own exchanges)
-                    at.barrier();
-                    return Cut{key_logit((uint32_t)(cut >> 32)), (int)(uint32_t)cut};
-                }
+                if (fits && n_list > 0)
+                    return cut_of(n_list, by_mass, need - over);
                 n_a = ~0ull;  // (no place for them: on to a single value)
             }
         }
@@ -1245,8 +1328,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Place &at, int p
             const PickArgs g{r, n, has_k ? k : 0, has_p, p, mp, u, m, inv, z_all, at.turn};
             if (n <= SC_THREADS / 8)
                 pick_of_few<8>(a, g);
-            else if (n <= SC_FEW)
+            else if (n <= SC_THREADS / 2)
                 pick_of_few<2>(a, g);
+            else if (n <= SC_FEW)
+                pick_of_few<1>(a, g);
             else
                 pick_of_many(a, g);
             return;
@@ -1282,7 +1367,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Place &at, int p
         u64 s[1] = {__reduce_add_sync(0xffffffffu, n)};
         cluster_sums(s, at);
         if (s[0] > (u64)k)
-            cut = y.search(false, (u64)k, s[0], cut);
+            cut = y.search(false, (u64)k, cut);
         if (has_p) {
             u64 z[1] = {mass_of(cut)};
             cluster_sums(z, at);
@@ -1290,7 +1375,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Place &at, int p
         }
     }
     if (has_p)
-        cut = y.search(true, needed_mass(p, z_all), z_all, cut);
+        cut = y.search(true, needed_mass(p, z_all), cut);
     auto kept = [&](float l, int i) -> float {
         const float e = cut.keeps(l, i) ? y.e_fast(l) : 0.f;
         return l == m || e >= mp ? e : 0.f;
@@ -1355,50 +1440,85 @@ __device__ __forceinline__ Place place_of(int C)
     return at;
 }
 
+// Rows that most likely need a search: a top-p of all tokens with no min_p to bound it, or a top-k that the threads'
+// maxima give no bound for.  (256 rows of 131001 with settings of their own: 118 us; with all rows without a top-k
+// 135, with none but the large top-k 129.)
+__device__ __forceinline__ bool is_heavy(const SampleArgs &a, int r)
+{
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const bool p = a.top_p && a.top_p[r] < 1.f && !(a.min_p && a.min_p[r] > 0.f);
+    return ((k <= 0 && p) || k > SC_THREADS) && (!a.tau || a.tau[r] > 0.f);
+}
+
 // A row per cluster (with NV = 0 per CTA).
 template <typename T, int NV>
 __global__ void __launch_bounds__(SC_THREADS, 2)
     k_sample(const SampleArgs a, const int C, const int per_warp, const bool defer)
 {
     Place at = place_of(NV > 0 ? C : 1);
-    if (defer)
+    const int r = blockIdx.x / at.C;
+    if (defer) {
         pdl_launch_dependents();
-    sample_row<T, NV>(a, at, per_warp, blockIdx.x / at.C, defer);
+        if (is_heavy(a, r))
+            return;  // (the second kernel's)
+    }
+    sample_row<T, NV>(a, at, per_warp, r, defer);
 }
 
-// The rows that the kernel before left.  Every CTA of a cluster reads the
-// marks of its rows before any of them ends, which takes a barrier of all.
+// Beside the kernel before, the heavy rows, by turns over the clusters; after it, the rows that it left.  (All that
+// this kernel reads before it waits is older than that kernel, which was launched after all work before it.)  Every
+// CTA of a cluster reads the marks of its rows before any of them ends, which takes a barrier of all.
 template <typename T, int NV>
 __global__ void __launch_bounds__(SC_THREADS, 2)
-    k_sample_pending(const SampleArgs a, const int C, const int per_warp, const int T_rows)
+    k_sample_rest(const SampleArgs a, const int C, const int per_warp, const int T_rows)
 {
+    __shared__ unsigned s_rows[SC_WARPS];
     Place at = place_of(C);
     const int me = blockIdx.x / C, clusters = gridDim.x / C;
-    pdl_wait();
-    for (int r0 = 0; r0 < T_rows; r0 += 32) {
-        const int mark = r0 + at.lane < T_rows ? *(volatile int32_t *)(a.tokens + r0 + at.lane) : 0;
-        unsigned left = __ballot_sync(0xffffffffu, mark <= PENDING && (PENDING - mark) % clusters == me);
-        for (; left; left &= left - 1) {
-            sample_row<T, NV>(a, at, per_warp, r0 + __ffs(left) - 1, false);
+    int turn = 0;
+#pragma unroll 1
+    for (int left = 0; left < 2; ++left) {
+        if (left)
+            pdl_wait();
+        for (int r0 = 0; r0 < T_rows; r0 += SC_THREADS) {
+            const int r = r0 + threadIdx.x;
+            bool is = r < T_rows && is_heavy(a, r) == !left;
+            if (is && left) {
+                const int mark = *(volatile int32_t *)(a.tokens + r);
+                is = mark <= PENDING && (PENDING - mark) % clusters == me;
+            }
+            const unsigned rows = __ballot_sync(0xffffffffu, is);
+            if (at.lane == 0)
+                s_rows[at.warp] = rows;
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < SC_WARPS; ++w)
+#pragma unroll 1
+                for (unsigned m = s_rows[w]; m; m &= m - 1) {
+                    if (!left && turn++ % clusters != me)
+                        continue;
+                    sample_row<T, NV>(a, at, per_warp, r0 + w * 32 + __ffs(m) - 1, false);
+                    __syncthreads();
+                }
             __syncthreads();
         }
     }
 }
 
-enum { ROWS_ALL, ROWS_DEFER, ROWS_PENDING };
+enum { ROWS_ALL, ROWS_DEFER, ROWS_REST };
 
 template <typename T, int NV>
 cudaError_t launch_rows(const SampleArgs &a, int T_rows, int C, int per_warp, int rows, cudaStream_t st)
 {
     static thread_local int attr_dev[2] = {-1, -1};  // per host thread and kernel
-    const bool pending = rows == ROWS_PENDING;
+    const bool pending = rows == ROWS_REST;
     int dev = 0;
     cudaGetDevice(&dev);
     if (attr_dev[pending] != dev) {
         const void *f = reinterpret_cast<const void *>(k_sample<T, NV>);
         if constexpr (NV > 0)
             if (pending)
-                f = reinterpret_cast<const void *>(k_sample_pending<T, NV>);
+                f = reinterpret_cast<const void *>(k_sample_rest<T, NV>);
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
@@ -1425,7 +1545,7 @@ cudaError_t launch_rows(const SampleArgs &a, int T_rows, int C, int per_warp, in
     cfg.numAttrs = pending ? 2 : 1;
     if constexpr (NV > 0)
         if (pending)
-            return cudaLaunchKernelEx(&cfg, k_sample_pending<T, NV>, a, C, per_warp, T_rows);
+            return cudaLaunchKernelEx(&cfg, k_sample_rest<T, NV>, a, C, per_warp, T_rows);
     return cudaLaunchKernelEx(&cfg, k_sample<T, NV>, a, C, per_warp, rows == ROWS_DEFER);
 }
 
@@ -1447,9 +1567,10 @@ cudaError_t launch_cluster(const SampleArgs &a, int T_rows, int C, int vectors, 
 // The form.  A cluster: as few CTAs as hold a row in 16 or 32 registers a
 // thread, and while the rows leave SMs idle twice as many.  Where the
 // clusters would come in more than three rounds of two CTAs an SM, a CTA per
-// row that reads it again, and then clusters for the rows that it left (256
-// rows of 131072: 75 us in clusters, 21 us by CTAs); the CTAs alone where 16
-// do not hold a row.
+// row that reads it again, and beside and after it clusters for the heavy
+// rows and those that were left (256 rows of 131001 with settings of their
+// own: 128 us in clusters alone, 118 us so; with top-k 50 and top-p 0.95 in
+// all: 75 and 31 us); the CTAs alone where 16 do not hold a row.
 template <typename T>
 cudaError_t launch_sample(const SampleArgs &a, int T_rows, cudaStream_t st)
 {
@@ -1464,7 +1585,7 @@ cudaError_t launch_sample(const SampleArgs &a, int T_rows, cudaStream_t st)
         return launch_rows<T, 0>(a, T_rows, 1, per_warp, ROWS_ALL, st);
     if (C > 1 && (long long)T_rows * C > 6ll * sm_count()) {
         const cudaError_t e = launch_rows<T, 0>(a, T_rows, 1, per_warp, ROWS_DEFER, st);
-        return e == cudaSuccess ? launch_cluster<T>(a, T_rows, C, vectors, ROWS_PENDING, st) : e;
+        return e == cudaSuccess ? launch_cluster<T>(a, T_rows, C, vectors, ROWS_REST, st) : e;
     }
     while (C < SC_MAX_CLUSTER && vectors > C * SC_THREADS && (long long)T_rows * C * 2 <= sm_count())
         C *= 2;

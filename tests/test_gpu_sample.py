@@ -260,6 +260,63 @@ def test_nearly_flat_rows_keep_most_of_the_vocabulary():
         np.testing.assert_allclose(prob, [1.0 / cut] * 6, rtol=1e-2)  # (one token more or fewer shows above)
 
 
+def wide_enough(share):
+    """For long rows: tokens of 4e-6 of the mass and up, or 0.99 of the largest (at least 1.8e-6 here).  Half of that
+    is above 9e-7; the sums' error is below 5e-7 of the mass (a weight's 2^-22, sums of at most 32 in 32 bits)."""
+    return np.flatnonzero(share > min(4e-6, share.max() * 0.99))
+
+
+def middle_of_wide(l, tau, k, frac):
+    order = ordered(l)
+    order = order[:k] if k > 0 else order
+    e = np.exp((l[order] - l[order[0]]) / tau)
+    c = np.cumsum(e) / e.sum()
+    width = np.diff(np.concatenate([[0.0], c]))
+    wide = wide_enough(width)
+    at = wide[np.argmin(np.abs(c[wide] - frac))]
+    return float(c[at] - width[at] / 2)
+
+
+@pytest.mark.parametrize("T,V,dtype", [(256, 131001, torch.bfloat16), (240, 40000, torch.float32),
+                                       (3, 600001, torch.bfloat16), (5, (1 << 19) + 5, torch.float32)])
+def test_many_or_very_long_rows_end_at_the_cut(T, V, dtype):
+    """Rows in descending order, so that a u near 1 gives the cut itself."""
+    r = np.random.RandomState(T)
+    ls, rows = [], []
+    for t in range(T):
+        kind = t % 10
+        l = r.randn(V) * (2.5 if kind in (0, 1, 6) else 0.4)
+        if kind == 3:
+            l[:] = 1.25  # all alike
+        elif kind == 4:
+            l = np.where(r.rand(V) < 0.5, 0.0, -1.0)  # two values
+        elif kind == 5:
+            l[r.rand(V) < 0.9] = -np.inf
+        elif kind == 6:
+            l[:30] += 9
+        elif kind == 9:
+            l = r.randn(V) * 0.02
+        ls.append(-np.sort(-np.round(l * 256) / 256))
+        k = {7: 3000, 8: V // 2}.get(kind, 0)
+        rows.append((float(np.float32(r.uniform(0.5, 1.3))), k, [0.95, 0.8, 0.5, 0.999, 1.0][r.randint(5)],
+                     kind in (2, 6)))
+    logits, seen = as_seen(np.stack(ls), dtype)
+    settings, us, toks, shares = [], [], [], []
+    for l, (tau, k, frac, with_mp) in zip(seen, rows):
+        p = 1.0 if frac == 1.0 else float(np.float32(middle_of_wide(l, tau, k, frac)))
+        mp = float(np.float32(middle_min_p(l, tau, near=0.3))) if with_mp else 0.0
+        idx, e = kept(l, tau, k, p, mp)
+        share = e / e.sum()
+        at = wide_enough(share)[-1]
+        settings.append((tau, k, p, mp))
+        us.append(float(np.cumsum(share)[at] - share[at] / 2))
+        toks.append(idx[at])
+        shares.append(share[at])
+    got, prob = run(logits, us, *map(list, zip(*settings)))
+    np.testing.assert_array_equal(got, toks)
+    np.testing.assert_allclose(prob, shares, rtol=4e-6)
+
+
 def test_sample_refuses_what_it_cannot_take():
     import tenant_composite_lora_gb300 as tcl
     l, u = torch.zeros(4, 32, device="cuda"), torch.zeros(4, device="cuda")
