@@ -1,0 +1,149 @@
+"""A decode step of one attention layer whose requests share a system prompt
+and each bring adapters of their own.
+
+Per step, all of it on the device and captured once in a CUDA graph:
+
+    x = emb[tokens]
+    q, k, v = x Wq, x Wk, x Wv   (library products)  + the adapters' deltas
+    the cache takes k (rotated) and v; q is rotated
+    o = attention over the prompt, which is read once for all requests, and
+        over each request's own tokens
+    h = x + o Wo + the adapters' delta;  logits = h head
+    tokens = sampled from the logits, with settings per request
+
+    python -m examples.decode_step [--requests 32] [--prompt 1000] [--steps 16]
+"""
+from __future__ import annotations
+
+import argparse
+
+import numpy as np
+import torch
+
+import tenant_composite_lora_gb300 as tcl
+
+
+def _random(gen, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).to(torch.bfloat16)
+
+
+class DecodeStep:
+    """Weights, adapters, cache and plan of a batch of `requests` behind one
+    prompt of `prompt` tokens, each with up to `max_new` tokens of its own."""
+
+    def __init__(self, requests, prompt, max_new, hidden=512, hq=8, hkv=2, d=64, vocab=4001, page=16, adapters=6,
+                 r_max=8, seed=0):
+        gen = torch.Generator().manual_seed(seed)
+        B, self.B, self.hq, self.hkv, self.d, self.page = requests, requests, hq, hkv, d, page
+        widths = {"q": (hidden, hq * d), "k": (hidden, hkv * d), "v": (hidden, hkv * d), "o": (hq * d, hidden)}
+        self.emb = _random(gen, vocab, hidden).cuda()
+        self.head = _random(gen, hidden, vocab, scale=hidden ** -0.5).cuda()
+        gain = {"q": 1.4, "k": 1.4, "v": 1.0, "o": 4.0}
+        self.w = {n: _random(gen, i, o, scale=gain[n] * i ** -0.5).cuda() for n, (i, o) in widths.items()}
+        # the adapters, of ranks of their own, and each request's pair of them
+        self.ranks = torch.randint(1, r_max + 1, (adapters,), generator=gen).to(torch.int32)
+        self.factors, self.pools = {}, {}
+        for n, (i, o) in widths.items():
+            self.pools[n] = tcl.LoraPool(i, o, r_max, adapters)
+            self.factors[n] = []
+            for a in range(adapters):
+                A, Bf = _random(gen, i, r_max, scale=i ** -0.5), _random(gen, r_max, o, scale=gain[n] * r_max ** -0.5)
+                self.pools[n].register(a, A.cuda(), Bf.cuda(), int(self.ranks[a]))
+                self.factors[n].append((A, Bf))
+        self.ids = torch.stack([torch.randperm(adapters, generator=gen)[:2] for _ in range(B)]).to(torch.int32)
+        self.alpha = torch.rand(B, 2, generator=gen)
+        self.mapping = tcl.LoraMapping(B, 2 * B, adapters)
+        self.mapping.build(torch.arange(0, 2 * B + 1, 2, dtype=torch.int32).cuda(), self.ids.flatten().cuda(),
+                           self.alpha.flatten().cuda())
+        # pages in any order: the prompt's, then each request's
+        own, self.prompt_pages = -(-max_new // page), -(-prompt // page)
+        pages = torch.randperm(self.prompt_pages + B * own, generator=gen).to(torch.int32).cuda()
+        self.num_pages = pages.numel()
+        self.cache = tcl.LoraKvCache(self.num_pages, page, hkv, d)
+        self.prefix_pages = pages[:self.prompt_pages][None].contiguous()
+        self.own_pages = pages[self.prompt_pages:].view(B, own).contiguous()
+        self.plan = tcl.LoraAttnPlan(B, 1, B, self.prompt_pages, own, hq, hkv, d, page)
+        angle = np.arange(prompt + max_new)[:, None] * 10000.0 ** (-np.arange(0, d, 2) / d)[None]
+        self.rope = torch.as_tensor(np.concatenate([np.cos(angle), np.sin(angle)], 1)).float().cuda()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.q_offsets, self.group_offsets = torch.arange(B + 1, **i32), torch.tensor([0, B], **i32)
+        self.prefix_len = torch.tensor([prompt], **i32)
+        self.length = torch.zeros(B, **i32)  # own tokens in the cache
+        self.positions = torch.full((B,), prompt, **i32)
+        self.tokens = torch.randint(0, vocab, (B,), generator=gen).to(torch.int32).cuda()
+        self.temperature = (0.6 + 0.6 * torch.rand(B, generator=gen)).cuda()
+        self.top_k = torch.tensor([0, 40], dtype=torch.int32).repeat(B)[:B].cuda()
+        self.top_p = torch.full((B,), 0.95, device="cuda")
+        self.status = torch.zeros(1, **i32)
+        self.u = torch.rand(B, generator=gen).cuda()
+        # the prompt: keys and values of the base weights, whoever reads them
+        self.prompt = torch.randint(0, vocab, (prompt,), generator=gen).cuda()
+        x, t = self.emb[self.prompt], torch.arange(prompt, device="cuda")
+        slots = (self.prefix_pages[0, t // page] * page + t % page).to(torch.int32)
+        tcl.kv_append(self.cache, (x @ self.w["k"]).view(prompt, hkv, d), (x @ self.w["v"]).view(prompt, hkv, d),
+                      slots, t.to(torch.int32), self.rope, status=self.status)
+
+    def _deltas(self, *projections):
+        tcl.lora_delta_apply_multi([(x, y, self.pools[n].handle, None) for n, x, y in projections],
+                                   self.mapping.handle)
+
+    def step(self):
+        """One token further: returns the logits; the sampled tokens are in self.tokens."""
+        B, d = self.B, self.d
+        x = self.emb[self.tokens]
+        q, k, v = x @ self.w["q"], x @ self.w["k"], x @ self.w["v"]
+        self._deltas(("q", x, q), ("k", x, k), ("v", x, v))
+        page = torch.gather(self.own_pages, 1, (self.length // self.page).long()[:, None])[:, 0]
+        slots = page * self.page + self.length % self.page
+        q = tcl.kv_append(self.cache, k.view(B, self.hkv, d), v.view(B, self.hkv, d), slots, self.positions, self.rope,
+                          q=q.view(B, self.hq, d), status=self.status)
+        self.length += 1
+        self.positions += 1
+        self.plan.build(self.q_offsets, self.length, self.own_pages, B, self.num_pages, self.group_offsets,
+                        self.prefix_len, self.prefix_pages)
+        o = tcl.prefix_attention(q, self.cache, self.plan).view(B, self.hq * d)
+        h = torch.addmm(x, o, self.w["o"])
+        self._deltas(("o", o, h))
+        logits = h @ self.head
+        tcl.sample(logits, self.u, self.temperature, self.top_k, self.top_p, tokens=self.tokens)
+        return logits
+
+    def check(self):
+        """Raises if a step was given a slot, position, page or length that it could not take."""
+        bad = int(self.status.item()) | self.plan.status()
+        if bad:
+            raise RuntimeError(f"device status {bad:#x}")
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    ap.add_argument("--requests", type=int, default=32)
+    ap.add_argument("--prompt", type=int, default=1000)
+    ap.add_argument("--steps", type=int, default=16)
+    a = ap.parse_args()
+    m = DecodeStep(a.requests, a.prompt, a.steps + 4, hidden=4096, hq=32, hkv=8, d=128, vocab=32768)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):  # (libraries and workspaces, before the capture)
+            m.step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.step()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    out = []
+    begin.record()
+    for _ in range(a.steps):
+        m.u.uniform_()
+        graph.replay()
+        out.append(m.tokens.clone())
+    end.record()
+    end.synchronize()
+    m.check()
+    print(f"{a.requests} requests behind {a.prompt} tokens: {begin.elapsed_time(end) / a.steps * 1e3:.0f} us a step")
+    print("first request:", [int(t[0]) for t in out])
+
+
+if __name__ == "__main__":
+    main()
