@@ -594,9 +594,11 @@ lora_status lora_attn_plan_build(lora_attn_plan *plan, const int32_t *q_offsets_
  *   lse_dev : NULL, or device fp32 [TQ][n_q_heads]
  *   cache   : its page_size, n_kv_heads and head_dim those of the plan, its
  *             num_pages at least the num_pages of the plan's build
- * fp32 scores, softmax statistics and sums; the weights are rounded to bf16
- * for the product with v.  Stream-ordered, no allocation; calls sharing a
- * plan must not overlap in time (they share its workspace).
+ * fp32 scores, softmax statistics and sums; the weights of a prefix or a
+ * request with more than 16 rows (query tokens times the heads that share a
+ * key/value head) are rounded to bf16 for the product with v, the others to
+ * 16 bits.  Stream-ordered, no allocation; calls sharing a plan must not
+ * overlap in time (they share its workspace).
  */
 lora_status lora_prefix_attention(const void *q_dev, long long q_stride, void *out_dev, long long out_stride,
                                   float *lse_dev, const lora_kv_cache *cache, lora_attn_plan *plan, float scale,
@@ -627,8 +629,10 @@ lora_status lora_attn_plan_destroy(lora_attn_plan *plan);
  *   tokens_dev : device int32 [T]; -1 for a row without a logit above -inf
  *   probs_dev  : NULL, or device fp32 [T]: the token's share of the kept mass
  * 1 <= V <= LORA_MAX_VOCAB, row_stride >= V.  The masses are summed in 64-bit
- * fixed point (2^-40 of the largest token's), so the result does not depend
- * on the order of summation.  Stream-ordered, no allocation.
+ * fixed point (2^-40 of the largest token's; up to 32 neighbouring tokens in
+ * fp32 before that), so the result does not depend on the order in which
+ * threads arrive.  Tokens of less than 2^-40 of the largest one's weight have
+ * no mass.  Stream-ordered, no allocation.
  */
 #define LORA_TYPE_F32 0
 #define LORA_TYPE_BF16 1

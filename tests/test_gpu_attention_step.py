@@ -358,6 +358,31 @@ def test_scores_that_grow_along_the_keys(spread):
     b.check(out, lse, b.reference())
 
 
+@pytest.mark.parametrize("hq,hkv,d,page", SHAPES)
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_that_are_not_positive(hq, hkv, d, page, scale):
+    b = Batch([1] * 20 + [70], [3] * 10 + [50] * 10 + [90], [21], [400], hq, hkv, d, page, seed=6)
+    b.scale = scale
+    out, lse = b.run()
+    assert b.status == 0
+    b.check(out, lse, b.reference())
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(8, 2, 128, 16), (4, 4, 64, 64)])
+@pytest.mark.parametrize("q_len,suffix,sizes,prefix", [
+    ([1] * 90, [400] * 90, [60, 30], [1, 0]),             # one short wide segment a head beside a cache full of narrow ones
+    ([300, 260, 1], [2100, 2600, 1], [3], [40]),          # one narrow segment of a key
+    ([1] * 70 + [200], [0] * 70 + [200], [71], [2000]),   # wide ones alone
+    ([1] * 12, [900] * 12, [1] * 12, [700] * 12),         # narrow ones alone
+])
+def test_mixtures_of_few_and_many_rows(hq, hkv, d, page, q_len, suffix, sizes, prefix):
+    """The SMs are shared out between segments of few and of many rows, down to one SM for either."""
+    b = Batch(q_len, suffix, sizes, prefix, hq, hkv, d, page, seed=8)
+    out, lse = b.run()
+    assert b.status == 0
+    b.check(out, lse, b.reference())
+
+
 @pytest.mark.parametrize("n", [3, 40, 200])
 def test_later_tokens_do_not_reach_earlier_queries(n):
     """A later token's key and value of inf or NaN leave the queries before it unchanged."""
