@@ -250,13 +250,15 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     float32 [T] and top_k int32 [T], or None.  Returns tokens (int32 [T],
     allocated unless given); probs: None or float32 [T]."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype, shape = logits.dtype, logits.shape
+    if len(shape) != 2 or dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("sample: logits are 2-D, float32 or bfloat16")
-    T, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+    T, V = shape
+    row, one = logits.stride()
+    if V > 1 and one != 1:
         raise ValueError("sample: each row of logits must be contiguous")
     if tokens is None:
         tokens = torch.empty(T, dtype=torch.int32, device=logits.device)
-    lora_sample(logits, native.LORA_TYPE_F32 if logits.dtype == torch.float32 else native.LORA_TYPE_BF16,
-                logits.stride(0) if T > 1 else V, T, V, u, temperature, top_k, top_p, min_p, tokens, probs, stream)
+    lora_sample(logits, native.LORA_TYPE_F32 if dtype == torch.float32 else native.LORA_TYPE_BF16,
+                row if T > 1 else V, T, V, u, temperature, top_k, top_p, min_p, tokens, probs, stream)
     return tokens

@@ -6,8 +6,9 @@ and h; the reference rounds its 64-bit values there too, since a rounded score
 between two strong keys moves o by several per cent.  What is left is a value
 now and then that rounds the other way, and the weights' rounding: 2^-4 of the
 logits' rms bounds them, and 2^-8 of a logit its own rounding.  The mistakes
-that the step could make (adapters, rotation or prompt left out) move logits by
-more than 2^-2 of the rms, which the test shows on the reference.
+that the step could make (adapters, rotation or prompt left out) move logits of
+some request by more than 2^-2 of the rms, which the test shows on the
+reference, early, while the prompt outweighs the requests' own tokens.
 """
 import numpy as np
 import pytest
@@ -95,7 +96,7 @@ def interval(l, tau, k, p, token):
 def test_steps_match_the_reference(requests, prompt, heads):
     from examples.decode_step import DecodeStep
     m = DecodeStep(requests, prompt, 20, vocab=1003, hidden=256, **heads)
-    ref = Reference(m)
+    ref, draw = Reference(m), torch.Generator().manual_seed(requests)
     wrong = [Reference(m, **{x: False}) for x in ("adapters", "rotation", "prompt")]
     for step in range(18):  # over the end of a page
         tokens = m.tokens.cpu()
@@ -104,7 +105,7 @@ def test_steps_match_the_reference(requests, prompt, heads):
         want = ref.step(tokens)
         rms = float(want.square().mean().sqrt())
         assert float(((logits - want).abs() - 2 ** -8 * want.abs()).max()) < 2 ** -4 * rms
-        if step in (3, 17):
+        if step == 3 and requests > 1:
             for w in wrong:
                 w.k, w.v, w.at = list(ref.k[:-1]), list(ref.v[:-1]), ref.at - 1
                 assert float((w.step(tokens) - want).abs().max()) > 2 ** -2 * rms
@@ -112,7 +113,7 @@ def test_steps_match_the_reference(requests, prompt, heads):
             lo, hi = interval(logits[b].numpy(), *(float(x[b]) for x in (m.temperature,)), int(m.top_k[b]),
                               float(m.top_p[b]), token)
             assert lo - 1e-5 <= float(m.u[b]) <= hi + 1e-5
-        m.u.uniform_()
+        m.u.copy_(torch.rand(requests, generator=draw))
 
 
 def test_a_captured_step_gives_the_same_tokens():
