@@ -535,17 +535,26 @@ def _raw_stream() -> int:
     return _current_stream()
 
 
-def _array(fn: str, name: str, t, kind: str, want: int):
-    """``_need`` and ``_dptr`` of a tensor that passes both, in one look."""
-    if t is None:
-        return None
-    try:
-        if t.is_cuda and t.dtype == _types[kind] and t.is_contiguous() and t.numel() >= want:
-            return t.data_ptr()
-    except (AttributeError, KeyError):
-        pass
-    _need(fn, name, t, want)
-    return _dptr(t, name, kind)
+def _arrays(fn: str, *arrays):
+    """Addresses of device arrays, given as (name, array, kind, entries needed):
+    ``_need`` of each and then ``_dptr`` of each, for tensors that pass both in
+    one look."""
+    out = []
+    for _, t, kind, want in arrays:
+        if t is None:
+            out.append(None)
+            continue
+        try:
+            if not (t.is_cuda and t.dtype == _types[kind] and t.is_contiguous() and t.numel() >= want):
+                break
+            out.append(t.data_ptr())
+        except (AttributeError, KeyError):
+            break
+    else:
+        return out
+    for name, t, _, want in arrays:
+        _need(fn, name, t, want)
+    return [_dptr(t, name, kind) for name, t, kind, _ in arrays]
 
 
 def _rows_ptr(t, name: str, T: int, heads: int, d: int):
@@ -589,12 +598,11 @@ def lora_kv_append(cache: int, k, k_stride: int, v, v_stride: int, q, q_stride: 
     tensors or addresses."""
     fn = "lora_kv_append"
     turned = rot_dim > 0
-    s = load().lora_kv_append(cache, k, k_stride, v, v_stride, q, q_stride, q_out, out_stride, n_q_heads,
-                              _array(fn, "slots", slots, "int32", T),
-                              _array(fn, "positions", positions, "int32", T if turned else 0),
-                              _array(fn, "rope", rope, "float32", max_position * rot_dim if turned else 0),
-                              max_position, rot_dim, style, T, _array(fn, "status", status, "int32", 1),
-                              _fast_stream(stream))
+    slots, positions, rope, status = _arrays(
+        fn, ("slots", slots, "int32", T), ("positions", positions, "int32", T if turned else 0),
+        ("rope", rope, "float32", max_position * rot_dim if turned else 0), ("status", status, "int32", 1))
+    s = load().lora_kv_append(cache, k, k_stride, v, v_stride, q, q_stride, q_out, out_stride, n_q_heads, slots,
+                              positions, rope, max_position, rot_dim, style, T, status, _fast_stream(stream))
     if s:
         _check(fn, s)
 
@@ -634,8 +642,8 @@ def lora_prefix_attention(q, q_stride: int, out, out_stride: int, lse, cache: in
                           stream=None):
     """q, out: addresses (see ``_rows_ptr``)."""
     fn = "lora_prefix_attention"
-    s = load().lora_prefix_attention(q, q_stride, out, out_stride, _array(fn, "lse", lse, "float32", 0), cache, plan,
-                                     scale, _fast_stream(stream))
+    lse, = _arrays(fn, ("lse", lse, "float32", 0))
+    s = load().lora_prefix_attention(q, q_stride, out, out_stride, lse, cache, plan, scale, _fast_stream(stream))
     if s:
         _check(fn, s)
 
@@ -662,11 +670,10 @@ def lora_sample(logits, logits_type: int, row_stride: int, T: int, V: int, u, te
             raise ValueError(f"logits: elements of logits_type {logits_type} expected, got {logits.dtype}")
         logits = logits.data_ptr()
     f32 = "float32"
-    s = load().lora_sample(logits, logits_type, row_stride, T, V, _array(fn, "u", u, f32, T),
-                           _array(fn, "temperature", temperature, f32, T), _array(fn, "top_k", top_k, "int32", T),
-                           _array(fn, "top_p", top_p, f32, T), _array(fn, "min_p", min_p, f32, T),
-                           _array(fn, "tokens", tokens, "int32", T), _array(fn, "probs", probs, f32, T),
-                           _fast_stream(stream))
+    arrays = _arrays(fn, ("u", u, f32, T), ("temperature", temperature, f32, T), ("top_k", top_k, "int32", T),
+                     ("top_p", top_p, f32, T), ("min_p", min_p, f32, T), ("tokens", tokens, "int32", T),
+                     ("probs", probs, f32, T))
+    s = load().lora_sample(logits, logits_type, row_stride, T, V, *arrays, _fast_stream(stream))
     if s:
         _check(fn, s)
 
