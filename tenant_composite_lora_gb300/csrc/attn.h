@@ -24,8 +24,11 @@ constexpr int ATTN_BOX_MAX = 64;
 // the same for every key/value head.
 //
 // Groups and requests of at most NA_ROWS rows go to the narrow kernel (tiles
-// of 16 rows and 16 keys, a run of tiles per warp), the others to the wide
-// one (256 rows, 128 keys, a run per CTA).  Of each class, all tiles of all
+// of 16 rows and 16 keys, a run of tiles per warp: such rows fill one product
+// of 16 rows, and the keys are read once), the others to the wide one (256
+// rows, 128 keys, a run per CTA).  All of them in the wide kernel: 32 requests
+// behind 4099 keys 34 us for 23, 256 behind 32768 keys 250 for 159, 64 in 16
+// groups 104 for 77.  Of each class, all tiles of all
 // segments and heads stand in one sequence, segment by segment, head by head,
 // in the order of the keys, each head's tiles after a lead of units that
 // stands for what beginning and ending a piece costs; each worker takes an
@@ -71,7 +74,7 @@ enum { AL_UNITS = 0, AL_RUN = 1, AL_PART = 2, AL_CTAS = 3, AL_WORDS = 4 };
 // it, and the two kernels run side by side -- the narrow one waits for the cache's bytes, the wide one for its
 // products.  Measured, 32 requests behind 4099 keys, 256 behind 32768, 64 in 16 groups (head_dim 128) and 24
 // with 8 tokens each (head_dim 64): 24, 161, 78 and 31 us; each kernel on all SMs, one after the other:
-// 29, 162, 92 and 35 us; 30 % more or less for the narrow one: up to 15 % more.
+// 29, 162, 92 and 35 us; the narrow unit a third cheaper: 24, 221, 82 and 32 us.
 __host__ __device__ constexpr int attn_unit_ns(int cls, int d)
 {
     return cls == AC_WIDE ? (d == 64 ? 1100 : 1950) : (d == 64 ? 52 : 105);

@@ -4,7 +4,9 @@
 // A rotation mixes the pairs (a, b) of a head's first rot_dim elements:
 //     a' = a c - b s,  b' = b c + a s,   c, s = rope[position][i], rope[position][rot_dim / 2 + i],
 // in fp32, rounded once to bf16.  Pure movement: every element is read and
-// written once.
+// written once.  Bound by the bytes for long batches (3250 tokens of 32 + 8
+// heads of 128, 82 MB: 15.7 us, 5.2 TB/s of 6.8 measured for a copy), by the
+// launch for short ones (1 token 2.4 us, 256 tokens 2.8 us).
 #include <cstdlib>
 
 #include "attn.h"
@@ -32,7 +34,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
 }
 
 // A thread moves two 16-byte chunks of one head of one token: with halves
-// style in the rotated part a chunk and the one rot / 2 elements on.
+// style in the rotated part a chunk and the one rot / 2 elements on, so that
+// no pair is exchanged between threads and every load is on its way at once.
 template <bool HALVES>
 __global__ void __launch_bounds__(256) k_kv_append(const AppendArgs a)
 {
